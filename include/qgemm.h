@@ -10,6 +10,7 @@
  *         zero = 0, the scale-only forms of acext 1.3.2)
  *   int8, per channel: W[n, k] = q[n, k] * scale[n]
  *   int8, groupwise:   W[n, k] = q[n, k] * scale[n, k/g]   (no zero)
+ *   MX4 (4-bit floats): W[n, k] = value(code[n, k]) * 2^(scale[n, k/32] - 127)
  *
  * Sources: "acext User Guide (v1.7)", 1.2.1 fpAintB GEMM (argument set: A,
  * B, scales, zero points, biases, C, m, n, k, group size, workspace, stream),
@@ -309,6 +310,101 @@ qg_status qembed_w4(const int32_t *ids, int tokens, const uint8_t *table, int la
 qg_status qembed_w8(const int32_t *ids, int tokens, const int8_t *table, int layout,
                     const void *scales, void *out, int vocab, int hidden, int group_size,
                     qg_dtype act_dtype, qg_dtype out_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floats (MX4).  A code is a 4-bit float: bit 3 the sign,
+ * bits 0-2 the magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6.  32 consecutive values
+ * of a row (a block) share one scale byte s that stands for 2^(s - 127), 255
+ * for NaN:  value = magnitude(code) * 2^(s - 127).  0.53 bytes per value.
+ * (The OCP Microscaling Formats specification's MXFP4; the pages describe no
+ * floating-point weight format.)
+ *
+ * Portable layout (any rows, k % 32 == 0):
+ *     codes   uint8 [rows, k/2], byte j of a row = c[2j] | c[2j+1] << 4
+ *     scales  uint8 [rows, k/32]
+ * Tiled layout (k % 128 == 0), the order the matrix instructions read, with
+ * rows padded to a multiple of 16, R = 16 * ceil(rows / 16):
+ *     codes   uint8 [R, k/2]: 1024-byte blocks, one per (16 rows) x (128 k);
+ *             code (r, c) in block (r / 16) * (k / 128) + c / 128, there in
+ *             byte lane * 16 + (c % 32) / 2, nibble c % 2 (0 = low), with
+ *             lane = 16 * ((c % 128) / 32) + r % 16
+ *     scales  uint8 [R/16, ceil(k/512), 64, 4]: the scale of (r, block b) at
+ *             [r / 16][b / 16][16 * (b % 4) + r % 16][(b / 4) % 4]
+ *     Padding rows hold code 0 and scale 0, unused scale bytes 0.
+ * Tiled matrices of whole 16-row tiles stacked one after the other are the
+ * tiled form of the stacked matrix (so experts can be laid out in one call).
+ *
+ * qquantize_mx4: X [rows, k] -> codes and scales.  With a the block's largest
+ * magnitude:  s = max(floor(log2 a) - 2 + 127, 0); the code is x / 2^(s-127)
+ * rounded to the nearest magnitude, ties to the even code, values beyond 6 to
+ * 6, the sign kept (also of a zero).  A block holding a NaN or an infinity
+ * gets s = 255 and codes 0: all its values read back as NaN.  Bit-exact by
+ * contract.
+ *   X        device [rows, k], QG_BF16, QG_FP16 or QG_FP32
+ *   layout   QG_LAYOUT_PORTABLE or QG_LAYOUT_TILED, of codes and scales
+ * qdequant_mx4: codes and scales -> out [rows, k] in out_dtype (QG_BF16,
+ * QG_FP16 or QG_FP32): the value rounded to nearest even (bf16 and fp32 hold
+ * every value but those of 2^128 and above, which round to infinity; fp16
+ * also rounds below 2^-23).  rows counts the valid rows; padding rows of the
+ * tiled layout are not written to out.
+ * qrepack_mx4 / qunrepack_mx4: portable -> tiled and back, exact inverses.
+ *   rows == 0 or k == 0: no-op.  Alignment: X, out and codes 16 bytes,
+ *   scales 4 (tiled) or 1 (portable).  Inputs and outputs must not overlap.
+ * ---------------------------------------------------------------------- */
+qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k, int layout,
+                        qg_dtype x_dtype, void *stream);
+qg_status qdequant_mx4(const uint8_t *codes, const uint8_t *scales, void *out, int rows, int k,
+                       int layout, qg_dtype out_dtype, void *stream);
+qg_status qrepack_mx4(const uint8_t *codes, const uint8_t *scales, uint8_t *codes_tiled,
+                      uint8_t *scales_tiled, int rows, int k, void *stream);
+qg_status qunrepack_mx4(const uint8_t *codes_tiled, const uint8_t *scales_tiled, uint8_t *codes,
+                        uint8_t *scales, int rows, int k, void *stream);
+
+/* MX4 products, B tiled [n, k], fp32 accumulation, C = RNE_out(sum + bias):
+ * qgemm_mx4a16:  C[m, n] = sum_k A[m, k] * W[n, k] (+ bias[n])
+ *   A        device [m, k] in act_dtype (QG_BF16 or QG_FP16)
+ *   C        device [m, n] in act_dtype; written, never read
+ *   W is value(B) in act_dtype: exact in bf16; in fp16 rounded as by
+ *   qdequant_mx4 (exact for values of 2^-23 and above, below 65520).
+ * qgemm_mx4a4:  C[m, n] = sum_k value(A)[m, k] * W[n, k] (+ bias[n])
+ *   A        codes and scales of the activations, tiled, m rows (padded to 16)
+ *   C        device [m, n] in out_dtype (QG_BF16, QG_FP16 or QG_FP32)
+ *   The products are exact, also across scales.
+ * qgemm_mx4a16_grouped:  rows offsets[e] .. offsets[e+1] - 1 of A times
+ *   expert e's weight (rows sorted by expert, any number of rows each):
+ *       C[r, n] = sum_k A[r, k] * W_e[n, k] (+ bias[e, n])
+ *   offsets  device int32 [experts + 1], non-decreasing, in [0, rows]
+ *            (values outside are read as the nearest bound, a decrease as
+ *            no rows: nothing outside the buffers is touched, but C is then
+ *            unspecified).  Rows before offsets[0] and from offsets[experts]
+ *            on are left as they were.
+ *   B        experts consecutive tiled [n, k] matrices; bias [experts, n]
+ *   experts  1 .. 65536
+ * Common: bias in bias_dtype (QG_BF16 or QG_FP16), or NULL with QG_NONE.
+ *   Tile multiples: n % 16 == 0, k % 128 == 0; m and rows any value >= 0.
+ *   Alignment: A, B, C 16 bytes, scales and offsets 4, bias 2.
+ *   A NaN scale makes NaN of the outputs that read it.
+ *   workspace: optional device scratch, 256-byte aligned.  With at least
+ *   qgemm_mx4_workspace_size(m, n, k, act_bits) bytes (act_bits 16 or 4; > 0
+ *   for problems with few tiles) K slices write fp32 partials [slices, m, n]
+ *   there and one more launch sums them in slice order; with less (or NULL)
+ *   the same call runs unsplit.  Calls that share a workspace must not
+ *   overlap. */
+size_t qgemm_mx4_workspace_size(int m, int n, int k, int act_bits);
+
+qg_status qgemm_mx4a16(const void *A, const uint8_t *B_tiled, const uint8_t *B_scales,
+                       const void *bias, void *C, int m, int n, int k, qg_dtype act_dtype,
+                       qg_dtype bias_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+qg_status qgemm_mx4a4(const uint8_t *A_tiled, const uint8_t *A_scales, const uint8_t *B_tiled,
+                      const uint8_t *B_scales, const void *bias, void *C, int m, int n, int k,
+                      qg_dtype out_dtype, qg_dtype bias_dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+qg_status qgemm_mx4a16_grouped(const void *A, const int32_t *offsets, const uint8_t *B_tiled,
+                               const uint8_t *B_scales, const void *bias, void *C, int rows, int n,
+                               int k, int experts, qg_dtype act_dtype, qg_dtype bias_dtype,
+                               void *stream);
 
 /* ------------------------------------------------------------------------
  * Top-k MoE with SiLU-gated int4 experts  (acext User Guide (v1.7), 1.2.3

@@ -22,7 +22,8 @@ __all__ = [
     "unrepack_w8_kn", "quantize_w4", "dequant_w4", "dequant_w8", "gemm_w4a16", "gemm_w8a16",
     "moe_grouped", "moe_workspace_size", "gemm_workspace_size", "dtype_code", "gemm_w8a8",
     "w8a8_workspace_size", "embed_w4", "embed_w8", "read_probe", "lds_probe", "set_override", "clear_override",
-    "moe_grouped_noalloc",
+    "moe_grouped_noalloc", "quantize_mx4", "dequant_mx4", "repack_mx4", "unrepack_mx4",
+    "gemm_mx4a16", "gemm_mx4a4", "gemm_mx4a16_grouped", "mx4_workspace_size",
 ]
 
 _CODES = {torch.bfloat16: QG_BF16, torch.float16: QG_FP16, torch.float32: QG_FP32}
@@ -458,6 +459,224 @@ def embed_w8(ids: torch.Tensor, table: torch.Tensor, scales: torch.Tensor, group
         _ptr(scales), _ptr(out), vocab, hidden, group_size, dtype_code(scales.dtype),
         dtype_code(out.dtype), _stream(table)))
     return out
+
+
+# -- microscaled 4-bit floats (MX4) ----------------------------------------------
+
+_U8 = torch.uint8
+
+
+def _mx4_tiled_shapes(rows: int, k: int) -> tuple:
+    """Shapes of the tiled codes and scales of [rows, k]."""
+    rt = (rows + 15) // 16
+    return (rt * 16, k // 2), (rt, (k + 511) // 512, 64, 4)
+
+
+def _mx4_multiple(func: str, k: int, step: int) -> None:
+    _need(k % step == 0, func, 7, f"k must be a multiple of {step} (got {k})")
+
+
+def _mx4_devices(func: str, *named) -> int:
+    """The device index the given (tensor, name) pairs share; None is skipped."""
+    dev = None
+    for t, name in named:
+        if t is None:
+            continue
+        _dev(t, name)
+        if dev is None:
+            dev = t.get_device()
+        _need(t.get_device() == dev, func, _SHAPE, f"{name} must be on cuda:{dev} like the others")
+    return dev
+
+
+def _mx4_call(func: str, dev: int, *args) -> None:
+    """The library call, with the tensors' device as the current one."""
+    fn = getattr(lib(), func)
+    if dev == torch.cuda.current_device():
+        check(func, fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            check(func, fn(*args))
+
+
+def _check_mx4_pair(func: str, codes: torch.Tensor, scales: torch.Tensor, tiled: bool,
+                    names=("codes", "scales"), lead: tuple = ()) -> tuple:
+    """(rows held, k) of a codes / scales pair (after the leading dimensions)."""
+    nd = len(lead) + 2
+    _need(codes.dtype == _U8 and scales.dtype == _U8, func, _DTYPE,
+          f"{names[0]} and {names[1]} must be uint8")
+    _need(codes.dim() == nd and _shape(codes)[:-2] == lead, func, _SHAPE,
+          f"{names[0]} must be {list(lead)} + [rows, k/2] (got {list(codes.shape)})")
+    rows, k = codes.shape[-2], 2 * codes.shape[-1]
+    if tiled:
+        _need(rows % 16 == 0, func, 7, f"{names[0]} must hold whole 16-row tiles (got {rows} rows)")
+        _mx4_multiple(func, k, 128)
+        want = lead + _mx4_tiled_shapes(rows, k)[1]
+    else:
+        _mx4_multiple(func, k, 32)
+        want = lead + (rows, k // 32)
+    _need(_shape(scales) == want, func, _SHAPE,
+          f"{names[1]} must be {list(want)} (got {list(scales.shape)})")
+    return rows, k
+
+
+def quantize_mx4(X: torch.Tensor, tiled: bool = False):
+    """MX4 quantization of X [..., k] (bf16, fp16 or fp32), leading dimensions
+    flattened to rows: (codes, scales) in the portable layout (uint8
+    [rows, k/2] and [rows, k/32]) or, tiled, in the layout the products take
+    (rows padded to 16; uint8 [R, k/2] and [R/16, ceil(k/512), 64, 4])."""
+    f = "qquantize_mx4"
+    _need(X.dtype in _CODES and X.dim() >= 1, f, _DTYPE, f"X must be bf16, fp16 or fp32 (got {X.dtype})")
+    k = X.shape[-1]
+    _mx4_multiple(f, k, 128 if tiled else 32)
+    dev = _mx4_devices(f, (X, "X"))
+    rows = X.numel() // k if k else 0
+    shapes = _mx4_tiled_shapes(rows, k) if tiled else ((rows, k // 2), (rows, k // 32))
+    codes = torch.empty(shapes[0], dtype=_U8, device=X.device)
+    scales = torch.empty(shapes[1], dtype=_U8, device=X.device)
+    _mx4_call(f, dev, _ptr(X), _ptr(codes), _ptr(scales), rows, k,
+              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[X.dtype], _stream(X))
+    return codes, scales
+
+
+def dequant_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+                tiled: bool = False, rows: Optional[int] = None) -> torch.Tensor:
+    """MX4 codes and scales -> values [rows, k] in out_dtype.  rows: how many
+    of the rows held are wanted (tiled matrices pad them to 16; default all)."""
+    f = "qdequant_mx4"
+    _need(out_dtype in _CODES, f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
+    held, k = _check_mx4_pair(f, codes, scales, tiled)
+    rows = held if rows is None else rows
+    _need(0 <= rows <= held, f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
+    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
+    out = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
+    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(out), rows, k,
+              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[out_dtype], _stream(codes))
+    return out
+
+
+def repack_mx4(codes: torch.Tensor, scales: torch.Tensor):
+    """Portable MX4 (codes, scales) -> tiled (codes, scales), rows padded to 16."""
+    f = "qrepack_mx4"
+    rows, k = _check_mx4_pair(f, codes, scales, False)
+    _mx4_multiple(f, k, 128)
+    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
+    shapes = _mx4_tiled_shapes(rows, k)
+    tc = torch.empty(shapes[0], dtype=_U8, device=codes.device)
+    ts = torch.empty(shapes[1], dtype=_U8, device=codes.device)
+    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(tc), _ptr(ts), rows, k, _stream(codes))
+    return tc, ts
+
+
+def unrepack_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: Optional[int] = None):
+    """Tiled MX4 (codes, scales) -> portable, the first `rows` rows (default all held)."""
+    f = "qunrepack_mx4"
+    held, k = _check_mx4_pair(f, codes, scales, True)
+    rows = held if rows is None else rows
+    _need(0 <= rows <= held, f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
+    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
+    pc = torch.empty((rows, k // 2), dtype=_U8, device=codes.device)
+    ps = torch.empty((rows, k // 32), dtype=_U8, device=codes.device)
+    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(pc), _ptr(ps), rows, k, _stream(codes))
+    return pc, ps
+
+
+def mx4_workspace_size(m: int, n: int, k: int, act_bits: int) -> int:
+    return int(lib().qgemm_mx4_workspace_size(m, n, k, act_bits))
+
+
+def _mx4_workspace(m: int, n: int, k: int, act_bits: int, device, given: Optional[torch.Tensor]):
+    if given is not None:
+        return given, given.numel() * given.element_size()
+    need = mx4_workspace_size(m, n, k, act_bits)
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=_U8, device=device), need
+
+
+def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C = A . value(B)^T (+ bias); A [..., k] bf16/fp16, B tiled MX4 [n, k]
+    (repack_mx4, or quantize_mx4 with tiled=True)."""
+    f = "qgemm_mx4a16"
+    _need(A.dtype in _ACT and A.dim() >= 1, f, _DTYPE, f"A must be bf16 or fp16 (got {A.dtype})")
+    n, k = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"))
+    _need(A.shape[-1] == k, f, _SHAPE, f"A must be [..., {k}] (got {list(A.shape)})")
+    _check_bias(f, bias, n)
+    m = A.numel() // k if k else 0
+    if out is not None:
+        _check_out(f, out, A.dtype, m, n)
+    dev = _mx4_devices(f, (A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
+                       (out, "out"), (workspace, "workspace"))
+    C = out if out is not None else torch.empty((m, n), dtype=A.dtype, device=A.device)
+    ws, ws_bytes = _mx4_workspace(m, n, k, 16, A.device, workspace)
+    _mx4_call(f, dev, _ptr(A), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C), m, n, k,
+              _CODES[A.dtype], dtype_code(None if bias is None else bias.dtype), _ptr(ws), ws_bytes,
+              _stream(A))
+    return C.reshape(*A.shape[:-1], n)
+
+
+def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Tensor,
+               B_scales: torch.Tensor, m: Optional[int] = None,
+               bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C [m, n] = value(A) . value(B)^T (+ bias), both tiled MX4.  m: the rows
+    of A that count (quantize_mx4 pads them to 16; default all held)."""
+    f = "qgemm_mx4a4"
+    held, k = _check_mx4_pair(f, A_tiled, A_scales, True, ("A_tiled", "A_scales"))
+    n, kb = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"))
+    _need(k == kb, f, _SHAPE, f"A_tiled and B_tiled must have the same k (got {k} and {kb})")
+    m = held if m is None else m
+    _need(0 <= m <= held, f, _SHAPE, f"m must be in [0, {held}] (got {m})")
+    _check_bias(f, bias, n)
+    if out is not None:
+        out_dtype = out.dtype
+        _check_out(f, out, out_dtype, m, n)
+    _need(out_dtype in _CODES, f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
+    dev = _mx4_devices(f, (A_tiled, "A_tiled"), (A_scales, "A_scales"), (B_tiled, "B_tiled"),
+                       (B_scales, "B_scales"), (bias, "bias"), (out, "out"), (workspace, "workspace"))
+    C = out if out is not None else torch.empty((m, n), dtype=out_dtype, device=A_tiled.device)
+    ws, ws_bytes = _mx4_workspace(m, n, k, 4, A_tiled.device, workspace)
+    _mx4_call(f, dev, _ptr(A_tiled), _ptr(A_scales), _ptr(B_tiled), _ptr(B_scales), _ptr(bias),
+              _ptr(C), m, n, k, _CODES[out_dtype], dtype_code(None if bias is None else bias.dtype),
+              _ptr(ws), ws_bytes, _stream(A_tiled))
+    return C
+
+
+def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.Tensor,
+                        B_scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of A
+    [rows, k] (bf16/fp16) times expert e's weight.
+
+    offsets int32 [E + 1], non-decreasing, on the device; B_tiled uint8
+    [E, n, k/2] and B_scales uint8 [E, n/16, ceil(k/512), 64, 4] (each expert
+    tiled; repack_mx4 of the experts stacked along n does them all); bias
+    [E, n].  Returns [rows, n]; rows of no expert are left as they were in
+    `out` (undefined without one).
+    """
+    f = "qgemm_mx4a16_grouped"
+    _need(A.dtype in _ACT and A.dim() == 2, f, _DTYPE, "A must be a 2-D bf16 or fp16 tensor [rows, k]")
+    _need(offsets.dtype == torch.int32, f, _DTYPE, f"offsets must be int32 (got {offsets.dtype})")
+    _need(offsets.dim() == 1 and offsets.numel() >= 2, f, _SHAPE, "offsets must be [E + 1], E >= 1")
+    E = offsets.numel() - 1
+    n, k = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"), lead=(E,))
+    rows = A.shape[0]
+    _need(A.shape[1] == k, f, _SHAPE, f"A must be [rows, {k}] (got {list(A.shape)})")
+    if bias is not None:
+        _need(bias.dtype in _ACT, f, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
+        _need(_shape(bias) == (E, n), f, _SHAPE, f"bias must be [{E}, {n}] (got {list(bias.shape)})")
+    if out is not None:
+        _check_out(f, out, A.dtype, rows, n)
+    dev = _mx4_devices(f, (A, "A"), (offsets, "offsets"), (B_tiled, "B_tiled"),
+                       (B_scales, "B_scales"), (bias, "bias"), (out, "out"))
+    C = out if out is not None else torch.empty((rows, n), dtype=A.dtype, device=A.device)
+    _mx4_call(f, dev, _ptr(A), _ptr(offsets), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C),
+              rows, n, k, E, _CODES[A.dtype], dtype_code(None if bias is None else bias.dtype),
+              _stream(A))
+    return C.reshape(rows, n)
 
 
 # -- measurement probe -----------------------------------------------------------

@@ -53,6 +53,14 @@ SIGNATURES = {
     "qg_read_probe_blocks": (_SZ, [_SZ]),
     "qg_read_probe": (_ST, [_P, _SZ, _P, _P]),
     "qg_lds_probe": (_ST, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P]),
+    "qquantize_mx4": (_ST, [_P, _P, _P, _INT, _INT, _INT, _INT, _P]),
+    "qdequant_mx4": (_ST, [_P, _P, _P, _INT, _INT, _INT, _INT, _P]),
+    "qrepack_mx4": (_ST, [_P, _P, _P, _P, _INT, _INT, _P]),
+    "qunrepack_mx4": (_ST, [_P, _P, _P, _P, _INT, _INT, _P]),
+    "qgemm_mx4_workspace_size": (_SZ, [_INT, _INT, _INT, _INT]),
+    "qgemm_mx4a16": (_ST, [_P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P, _SZ, _P]),
+    "qgemm_mx4a4": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P, _SZ, _P]),
+    "qgemm_mx4a16_grouped": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT, _P]),
     "qmoe_workspace_size": (_SZ, [_INT, _INT, _INT, _INT, _INT]),
     "qmoe_grouped": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT,
                            _INT, _P, _P, _P, _SZ, _P]),

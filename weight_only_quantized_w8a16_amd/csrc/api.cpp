@@ -318,6 +318,120 @@ qg_status qembed_w8(const int32_t *ids, int tokens, const int8_t *table, int lay
 }
 
 // ---------------------------------------------------------------------------
+// Microscaled 4-bit floats (MX4)
+// ---------------------------------------------------------------------------
+// Layout, multiples and alignment of the conversions (x: the 16- or 32-bit
+// side of a quantize or dequant, the portable codes of a repack).
+static qg_status mx4_layout_checks(const void *codes, const void *scales, const void *x, int rows,
+                                   int k, int layout) {
+  if (layout != QG_LAYOUT_PORTABLE && layout != QG_LAYOUT_TILED) return QG_ERR_MODE;
+  const bool tiled = layout == QG_LAYOUT_TILED;
+  if (k % (tiled ? 128 : 32) != 0 || rows > INT32_MAX - 15) return QG_ERR_UNSUPPORTED;
+  if (!aligned(codes, 16) || (tiled && !aligned(scales, 4)) || (x && !aligned(x, 16)))
+    return QG_ERR_ALIGN;
+  return QG_OK;
+}
+
+qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k, int layout,
+                        qg_dtype x_dt, void *stream) {
+  if (rows < 0 || k < 0) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;   // nothing to convert; pointers unused
+  if (!X || !codes || !scales) return QG_ERR_NULL;
+  if (!act_ok(x_dt) && x_dt != QG_FP32) return QG_ERR_DTYPE;
+  const qg_status st = mx4_layout_checks(codes, scales, X, rows, k, layout);
+  if (st != QG_OK) return st;
+  return hip_status(qg::launch_quantize_mx4(X, codes, scales, rows, k, layout == QG_LAYOUT_TILED,
+                                            static_cast<int>(x_dt), as_stream(stream)));
+}
+
+qg_status qdequant_mx4(const uint8_t *codes, const uint8_t *scales, void *out, int rows, int k,
+                       int layout, qg_dtype out_dt, void *stream) {
+  if (rows < 0 || k < 0) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;   // nothing to convert; pointers unused
+  if (!codes || !scales || !out) return QG_ERR_NULL;
+  if (!act_ok(out_dt) && out_dt != QG_FP32) return QG_ERR_DTYPE;
+  const qg_status st = mx4_layout_checks(codes, scales, out, rows, k, layout);
+  if (st != QG_OK) return st;
+  return hip_status(qg::launch_dequant_mx4(codes, scales, out, rows, k, layout == QG_LAYOUT_TILED,
+                                           static_cast<int>(out_dt), as_stream(stream)));
+}
+
+static qg_status mx4_repack_checks(const uint8_t *codes, const uint8_t *scales, const uint8_t *codes_t,
+                                   const uint8_t *scales_t, int rows, int k) {
+  if (rows < 0 || k < 0) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;
+  if (!codes || !scales || !codes_t || !scales_t) return QG_ERR_NULL;
+  return mx4_layout_checks(codes_t, scales_t, codes, rows, k, QG_LAYOUT_TILED);
+}
+
+qg_status qrepack_mx4(const uint8_t *codes, const uint8_t *scales, uint8_t *codes_t,
+                      uint8_t *scales_t, int rows, int k, void *stream) {
+  qg_status st = mx4_repack_checks(codes, scales, codes_t, scales_t, rows, k);
+  if (st != QG_OK || rows == 0 || k == 0) return st;
+  return hip_status(qg::launch_repack_mx4(codes, scales, codes_t, scales_t, rows, k, as_stream(stream)));
+}
+
+qg_status qunrepack_mx4(const uint8_t *codes_t, const uint8_t *scales_t, uint8_t *codes,
+                        uint8_t *scales, int rows, int k, void *stream) {
+  qg_status st = mx4_repack_checks(codes, scales, codes_t, scales_t, rows, k);
+  if (st != QG_OK || rows == 0 || k == 0) return st;
+  return hip_status(qg::launch_unrepack_mx4(codes_t, scales_t, codes, scales, rows, k, as_stream(stream)));
+}
+
+size_t qgemm_mx4_workspace_size(int m, int n, int k, int act_bits) {
+  if (m <= 0 || n <= 0 || k <= 0 || n % 16 != 0 || k % 128 != 0 || (act_bits != 16 && act_bits != 4))
+    return 0;
+  const size_t b = qg::mx4_workspace_bytes(m, n, k, act_bits);
+  return b ? (b + 255) & ~static_cast<size_t>(255) : 0;
+}
+
+static qg_status mx4_gemm(const void *A, const uint8_t *AS, const int32_t *offsets, const uint8_t *B,
+                          const uint8_t *BS, const void *bias, void *C, int m, int n, int k,
+                          int experts, bool a4, qg_dtype out, qg_dtype bias_dt, void *workspace,
+                          size_t ws_bytes, void *stream) {
+  const bool grouped = experts >= 0;
+  if (m < 0 || n < 0 || k <= 0 || (grouped && experts == 0)) return QG_ERR_SHAPE;
+  if (m == 0 || n == 0) return QG_OK;   // nothing to compute; pointers unused
+  if (!A || !B || !BS || !C || (a4 && !AS) || (grouped && !offsets)) return QG_ERR_NULL;
+  if (bias_dt != QG_NONE && !bias) return QG_ERR_NULL;
+  if (!act_ok(out) && !(a4 && out == QG_FP32)) return QG_ERR_DTYPE;
+  if (bias_dt == QG_NONE ? bias != nullptr : !act_ok(bias_dt)) return QG_ERR_DTYPE;
+  if (n % 16 != 0 || k % 128 != 0 || m > INT32_MAX - 255 || n > INT32_MAX - 255 ||
+      k > INT32_MAX - 511 || (grouped && experts > 65536))
+    return QG_ERR_UNSUPPORTED;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(BS, 4) ||
+      (AS && !aligned(AS, 4)) || (offsets && !aligned(offsets, 4)) || (bias && !aligned(bias, 2)))
+    return QG_ERR_ALIGN;
+  if (workspace && ws_bytes && !aligned(workspace, 256)) return QG_ERR_ALIGN;
+  const qg::Mx4Args a{A, AS, B, BS, static_cast<const uint16_t *>(bias), C, m, n, k,
+                      a4 ? qg::kMX4 : static_cast<int>(out), static_cast<int>(out), static_cast<int>(bias_dt), offsets,
+                      grouped ? experts : 0, workspace, workspace ? ws_bytes : 0};
+  return hip_status(qg::launch_mx4_gemm(a, as_stream(stream)));
+}
+
+qg_status qgemm_mx4a16(const void *A, const uint8_t *B, const uint8_t *BS, const void *bias, void *C,
+                       int m, int n, int k, qg_dtype act, qg_dtype bias_dt, void *workspace,
+                       size_t ws_bytes, void *stream) {
+  return mx4_gemm(A, nullptr, nullptr, B, BS, bias, C, m, n, k, -1, false, act,
+                  bias_dt, workspace, ws_bytes, stream);
+}
+
+qg_status qgemm_mx4a4(const uint8_t *A, const uint8_t *AS, const uint8_t *B, const uint8_t *BS,
+                      const void *bias, void *C, int m, int n, int k, qg_dtype out, qg_dtype bias_dt,
+                      void *workspace, size_t ws_bytes, void *stream) {
+  return mx4_gemm(A, AS, nullptr, B, BS, bias, C, m, n, k, -1, true, out, bias_dt, workspace,
+                  ws_bytes, stream);
+}
+
+qg_status qgemm_mx4a16_grouped(const void *A, const int32_t *offsets, const uint8_t *B,
+                               const uint8_t *BS, const void *bias, void *C, int rows, int n, int k,
+                               int experts, qg_dtype act, qg_dtype bias_dt, void *stream) {
+  if (experts < 0) return QG_ERR_SHAPE;
+  return mx4_gemm(A, nullptr, offsets, B, BS, bias, C, rows, n, k, experts, false, act,
+                  bias_dt, nullptr, 0, stream);
+}
+
+// ---------------------------------------------------------------------------
 // MoE
 // ---------------------------------------------------------------------------
 size_t qmoe_workspace_size(int tokens, int hidden, int inter, int experts, int topk) {

@@ -175,6 +175,39 @@ hipError_t launch_embed(const EmbedArgs &a, hipStream_t s);
 
 namespace qg {
 
+// Microscaled 4-bit floats (MX4).
+hipError_t launch_quantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k,
+                               int tiled, int x_dt, hipStream_t s);
+hipError_t launch_dequant_mx4(const uint8_t *codes, const uint8_t *scales, void *out, int rows,
+                              int k, int tiled, int out_dt, hipStream_t s);
+hipError_t launch_repack_mx4(const uint8_t *codes, const uint8_t *scales, uint8_t *codes_t,
+                             uint8_t *scales_t, int rows, int k, hipStream_t s);
+hipError_t launch_unrepack_mx4(const uint8_t *codes_t, const uint8_t *scales_t, uint8_t *codes,
+                               uint8_t *scales, int rows, int k, hipStream_t s);
+
+constexpr int kMX4 = 4;   // activation type code of MX4 activations (next to QG_BF16, QG_FP16)
+
+struct Mx4Args {
+  const void *A;             // [M, K] 16-bit, or tiled MX4 codes
+  const uint8_t *AS;         // tiled scales of A (MX4 activations), else null
+  const uint8_t *B, *BS;     // tiled codes and scales, [N, K] (per expert)
+  const uint16_t *bias;      // [N] (per expert) or null
+  void *C;                   // [M, N] in `out`
+  int M, N, K;
+  int act;                   // QG_BF16, QG_FP16 or kMX4
+  int out, bias_dt;
+  const int32_t *offsets;    // grouped: [E + 1] row offsets, else null
+  int E;                     // grouped: experts
+  void *ws;                  // split-K partials, may be null
+  size_t ws_bytes;
+};
+size_t mx4_workspace_bytes(int m, int n, int k, int act_bits);
+hipError_t launch_mx4_gemm(const Mx4Args &a, hipStream_t s);
+
+}  // namespace qg
+
+namespace qg {
+
 // Streaming-read probe (measurement).
 size_t read_probe_blocks(size_t bytes);
 hipError_t launch_read_probe(const void *buf, size_t bytes, uint32_t *out, hipStream_t s);
