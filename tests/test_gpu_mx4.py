@@ -142,6 +142,7 @@ def test_conversions_leave_neighbours_alone():
 
 # m, n, k: one row to several row tiles, one column tile to several, odd counts
 # of both, every remainder of k modulo 512
+KERNELS = ["stream", "T256", "T256N", "T128", "T64"]
 SHAPES = [(1, 16, 128), (1, 2048, 2048), (2, 48, 256), (3, 80, 384), (16, 272, 640), (17, 96, 512),
           (31, 528, 896), (64, 144, 1152), (100, 400, 1024), (129, 656, 768), (300, 272, 1664)]
 
@@ -272,6 +273,42 @@ def test_leading_dimensions_and_empty():
     assert qg.dequant_mx4(*q, tiled=True).shape == (0, 256)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_every_kernel_exact_sums(m, n, k, kernel):
+    # one kernel forced for sizes it would not be chosen for, too
+    qg.set_override(mx4_tile=kernel)
+    rng = np.random.default_rng(m + n + k)
+    codes, scales, _, _, a, w, bias, c = exact_case(rng, m, n, k, "a16")
+    for dtype in (BF, HF):
+        got = qg.gemm_mx4a16(torch.from_numpy(a).to(dtype).cuda(), *tiled(codes, scales), bias=dev(bias).to(BF))
+        same(got, ref.rne(c + bias, dtype))
+    codes, scales, ac, asc, a, w, bias, c = exact_case(rng, m, n, k, "a4")
+    for dtype in (BF, HF, SF):
+        got = qg.gemm_mx4a4(*tiled(ac, asc), *tiled(codes, scales), m=m, bias=dev(bias).to(HF), out_dtype=dtype)
+        same(got, ref.rne(c + bias, dtype))
+
+
+@pytest.mark.parametrize("kernel", ["T256", "T256N", "T128", "T64"])
+@pytest.mark.parametrize("m,n,k,slices", [(1, 16, 1024, 2), (70, 272, 1664, 4), (300, 144, 3584, 3)])
+def test_k_slices_exact_sums(m, n, k, slices, kernel):
+    # windows of 512 k shared out unevenly, the last slice and window partial;
+    # with less workspace the same call runs unsplit, to the same bits
+    qg.set_override(mx4_tile=kernel, mx4_split=slices)
+    rng = np.random.default_rng(m + k)
+    for act, bits in (("a16", 16), ("a4", 4)):
+        codes, scales, ac, asc, a, w, bias, c = exact_case(rng, m, n, k, act)
+        assert qg.mx4_workspace_size(m, n, k, bits) >= 2 * m * n * 4
+        for ws in (None, torch.empty(0, dtype=torch.uint8, device="cuda")):
+            if act == "a16":
+                got = qg.gemm_mx4a16(torch.from_numpy(a).to(BF).cuda(), *tiled(codes, scales),
+                                     bias=dev(bias).to(BF), workspace=ws)
+            else:
+                got = qg.gemm_mx4a4(*tiled(ac, asc), *tiled(codes, scales), m=m, bias=dev(bias).to(BF),
+                                    workspace=ws)
+            same(got, ref.rne(c + bias, BF))
+
+
 # -- grouped -----------------------------------------------------------------------
 
 SIZES = [[1], [0, 5, 0], [16, 0, 17, 1, 0], [3, 40, 130, 0, 0, 2], [0, 0, 0, 0],
@@ -306,7 +343,20 @@ def test_grouped_exact_sums(sizes, n, k, before, behind, dtype):
     same(out, ref.rne(c, dtype))   # rows of no expert keep their 9
 
 
-def test_grouped_bad_offsets_stay_inside():
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("sizes", [SIZES[2], SIZES[3], SIZES[6], SIZES[7]], ids=lambda s: f"{len(s)}x{sum(s)}")
+def test_grouped_every_kernel_exact_sums(sizes, kernel):
+    qg.set_override(mx4_tile=kernel)
+    a, off, B, S, bias, c = grouped_case(np.random.default_rng(len(sizes)), sizes, 272, 640, 2, 7)
+    for dtype in (BF, HF):
+        out = torch.full((a.shape[0], 272), 9.0, dtype=dtype, device="cuda")
+        qg.gemm_mx4a16_grouped(torch.from_numpy(a).to(dtype).cuda(), off, B, S, dev(bias).to(BF), out=out)
+        same(out, ref.rne(c, dtype))
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_grouped_bad_offsets_stay_inside(kernel):
+    qg.set_override(mx4_tile=kernel)
     # decreasing and out-of-range offsets: nothing outside the rows is written
     n, k, rows = 48, 256, 40
     rng = np.random.default_rng(2)

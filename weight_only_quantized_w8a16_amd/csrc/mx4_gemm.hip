@@ -14,6 +14,8 @@
 #include <algorithm>
 
 #include "mx4_common.hpp"
+#include "mx4_tile16.hpp"
+#include "mx4_tile4.hpp"
 
 namespace qg {
 
@@ -29,6 +31,8 @@ struct Mx4Problem {
   int M, N, K, bias_dt;
   const int32_t *offsets;
   int E;
+  float *part;           // K slices: fp32 partial sums [slices, M, N], else null
+  int kseg, slices;      // 512-k windows per slice, slices
 };
 
 // Inclusive prefix sum over the wave.
@@ -69,6 +73,17 @@ __device__ __forceinline__ bool group_tile(const int32_t *offsets, int E, int M,
     before = __shfl(upto, 63);
   }
   return false;
+}
+
+// Row tiles of BM rows of a grouped product.
+__device__ __forceinline__ int group_tiles(const int32_t *offsets, int E, int M, int BM) {
+  const int lane = threadIdx.x & 63;
+  int cnt = 0;
+  for (int x = lane; x < E; x += 64) {
+    const int lo = min(max(offsets[x], 0), M), hi = max(min(max(offsets[x + 1], 0), M), lo);
+    cnt += (hi - lo + BM - 1) / BM;
+  }
+  return __shfl(wave_scan(cnt, lane), 63);
 }
 
 template <int OUT>
@@ -159,6 +174,119 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tile kernels (mx4_tile16.hpp, mx4_tile4.hpp).
+// ---------------------------------------------------------------------------
+
+// Workgroup b runs on XCD b % 8.  Of `count` working workgroups each XCD takes
+// a contiguous run of the tile order, so neighbouring tiles share an L2.
+__device__ __forceinline__ int xcd_order(int b, int count) {
+  const int xcd = b & 7, loc = b >> 3, per = count >> 3, rem = count & 7;
+  return (xcd < rem) ? xcd * (per + 1) + loc : rem * (per + 1) + (xcd - rem) * per + loc;
+}
+
+// Where a finished sum goes: C, rounded with its bias, or a K slice's partials.
+template <int OUT, bool SPLIT>
+struct Mx4Store {
+  const Mx4Problem &p;
+  const uint16_t *bias;   // of the tile's expert
+  int slice;
+  __device__ __forceinline__ void operator()(int r, int col, const float (&v)[4]) const {
+    if constexpr (SPLIT) {
+      float *P = p.part + static_cast<size_t>(slice) * p.M * p.N;
+      *reinterpret_cast<f32x4 *>(P + static_cast<size_t>(r) * p.N + col) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      float o[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = bias ? v[x] + bits_to_f32_dyn(bias[col + x], p.bias_dt) : v[x];
+      store4<OUT>(p.C, static_cast<size_t>(r) * p.N + col, o);
+    }
+  }
+};
+
+// Row tile and column tile of this workgroup.  Dense: bands of four row tiles
+// walked column by column, so one weight tile serves the band's row tiles
+// while it is in L2.  Grouped: the column tiles of an expert's row tile next
+// to each other; the grid is sized for the most row tiles the offsets can
+// give, and workgroups past the real count end here.
+template <int BM, bool GROUPED>
+__device__ __forceinline__ bool mx4_tile_of(const Mx4Problem &p, int tiles_m, int tiles_n, int &tn, int &e,
+                                            int &slice, int &row0, int &row1) {
+  e = slice = 0;
+  if constexpr (GROUPED) {
+    const int count = group_tiles(p.offsets, p.E, p.M, BM) * tiles_n;
+    if (static_cast<int>(blockIdx.x) >= count) return false;
+    const int id = xcd_order(blockIdx.x, count), tm = id / tiles_n;
+    tn = id - tm * tiles_n;
+    return group_tile(p.offsets, p.E, p.M, BM, tm, e, row0, row1);
+  } else {
+    constexpr int G = 4;
+    int id = xcd_order(blockIdx.x, gridDim.x);
+    const int per = tiles_m * tiles_n;
+    slice = id / per;
+    id -= slice * per;
+    const int band = id / (G * tiles_n), first = band * G, gsz = min(G, tiles_m - first);
+    const int in = id - band * G * tiles_n;
+    tn = in / gsz;
+    row0 = (first + in % gsz) * BM;
+    row1 = min(p.M, row0 + BM);
+    return true;
+  }
+}
+
+template <class Cfg, int ACT, bool GROUPED, bool SPLIT>
+__global__ __launch_bounds__(Cfg::NTHR) void k_mx4_tile16(Mx4Problem p, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(16))) char a0[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char a1[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char a2[Cfg::NS > 2 ? Cfg::STAGE_A : 16];
+  __shared__ __attribute__((aligned(16))) char a3[Cfg::NS > 2 ? Cfg::STAGE_A : 16];
+  __shared__ __attribute__((aligned(16))) char b0[Cfg::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char b1[Cfg::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char b2[Cfg::NS > 2 ? Cfg::STAGE_B : 16];
+  __shared__ __attribute__((aligned(16))) char b3[Cfg::NS > 2 ? Cfg::STAGE_B : 16];
+  int tn, e, slice, row0, row1;
+  if (!mx4_tile_of<Cfg::BM, GROUPED>(p, tiles_m, tiles_n, tn, e, slice, row0, row1)) return;
+  const int nb = p.K >> 7, nw = mx4_scale_windows(p.K), ntiles = p.N >> 4, steps = p.K >> 6;
+  const Mx4Tile t{row0, row1 - 1, tn * Cfg::BN, SPLIT ? slice * p.kseg * 8 : 0,
+                  SPLIT ? min(steps, (slice + 1) * p.kseg * 8) : steps};
+  mx4_tile16<Cfg, ACT>(static_cast<const uint16_t *>(p.A), p.M, p.B + static_cast<size_t>(e) * ntiles * nb * 1024,
+                       p.BS + static_cast<size_t>(e) * ntiles * nw * 64, p.N, p.K, t,
+                       Mx4Lds{{a0, a1, a2, a3}, {b0, b1, b2, b3}},
+                       Mx4Store<ACT, SPLIT>{p, p.bias ? p.bias + static_cast<size_t>(e) * p.N : nullptr, slice});
+}
+
+template <class Cfg, int OUT, bool SPLIT>
+__global__ __launch_bounds__(Cfg::NTHR) void k_mx4_tile4(Mx4Problem p, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(16))) char a0[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char a1[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char a2[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char a3[Cfg::STAGE_A];
+  __shared__ __attribute__((aligned(16))) char b0[Cfg::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char b1[Cfg::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char b2[Cfg::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char b3[Cfg::STAGE_B];
+  int tn, e, slice, row0, row1;
+  if (!mx4_tile_of<Cfg::BM, false>(p, tiles_m, tiles_n, tn, e, slice, row0, row1)) return;
+  const int steps = p.K >> 7;
+  const Mx4Tile t{row0, row1 - 1, tn * Cfg::BN, SPLIT ? slice * p.kseg * 4 : 0,
+                  SPLIT ? min(steps, (slice + 1) * p.kseg * 4) : steps};
+  mx4_tile4<Cfg>(static_cast<const uint8_t *>(p.A), p.AS, p.M, p.B, p.BS, p.N, p.K, t,
+                 Mx4Lds{{a0, a1, a2, a3}, {b0, b1, b2, b3}}, Mx4Store<OUT, SPLIT>{p, p.bias, slice});
+}
+
+// K slices: C = RNE_out(the slices' partials summed in slice order + bias).
+template <int OUT>
+__global__ __launch_bounds__(256) void k_mx4_reduce(Mx4Problem p) {
+  const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
+  for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < mn; i += step) {
+    f32x4 s = *reinterpret_cast<const f32x4 *>(p.part + i);
+    for (int sl = 1; sl < p.slices; ++sl) s += *reinterpret_cast<const f32x4 *>(p.part + sl * mn + i);
+    const int r = static_cast<int>(i / p.N), col = static_cast<int>(i - static_cast<size_t>(r) * p.N);
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    Mx4Store<OUT, false>{p, p.bias, 0}(r, col, v);
+  }
+}
+
 namespace {
 
 constexpr int kMaxSlabs = 65535;   // grid.y
@@ -182,22 +310,134 @@ hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
 
 }  // namespace
 
-size_t mx4_workspace_bytes(int, int, int, int) { return 0; }
+namespace {
+
+using Cfg16L = Mx4Cfg16<256, 256, 2, 4, 4>;   // waves of 128 x 64
+using Cfg16N = Mx4Cfg16<256, 128, 4, 2, 4>;   // waves of 64 x 64
+using Cfg16M = Mx4Cfg16<128, 128, 2, 4, 4>;   // waves of 64 x 32
+using Cfg16S = Mx4Cfg16<64, 128, 2, 4, 4>;    // waves of 32 x 32
+using Cfg4L = Mx4Cfg4<256, 256, 2, 4, 4>;     // waves of 128 x 64
+using Cfg4N = Mx4Cfg4<256, 128, 4, 2, 4>;     // waves of 64 x 64
+using Cfg4M = Mx4Cfg4<128, 128, 2, 4, 4>;     // waves of 64 x 32
+using Cfg4S = Mx4Cfg4<64, 128, 2, 4, 4>;      // waves of 32 x 32
+
+struct Mx4Plan {
+  int tile;            // Mx4Tile order below, or kStream
+  int kseg, slices;    // K slices in 512-k windows
+  size_t bytes;        // partials
+};
+
+constexpr int tile_bm(int tile) { return tile == kMx4L || tile == kMx4N ? 256 : tile == kMx4M ? 128 : 64; }
+constexpr int tile_bn(int tile) { return tile == kMx4L ? 256 : 128; }
+
+Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
+  Mx4Plan pl{kMx4Stream, 0, 1, 0};
+  const Override ov = dispatch_override();
+  // 32-bit offsets of the tile kernels' buffer loads.
+  const uint64_t lim = uint64_t(1) << 31;
+  const uint64_t a_bytes = uint64_t((M + 15) / 16 * 16) * K / (a4 ? 2 : 1) * (a4 ? 1 : 2);
+  const bool fits = a_bytes < lim && uint64_t(N) * K / 2 < lim;
+  if (!fits || ov.mx4_tile == kMx4Stream) return pl;
+  if (ov.mx4_tile >= 0) pl.tile = ov.mx4_tile;
+  else if (M > 64) pl.tile = kMx4M;
+  if (pl.tile == kMx4Stream) return pl;
+  if (ov.mx4_split > 1 && !grouped) {
+    const int windows = mx4_scale_windows(K), want = std::min(ov.mx4_split, windows);
+    pl.kseg = (windows + want - 1) / want;
+    pl.slices = (windows + pl.kseg - 1) / pl.kseg;
+    if (pl.slices > 1) pl.bytes = static_cast<size_t>(pl.slices) * M * N * sizeof(float);
+  }
+  return pl;
+}
+
+template <int OUT>
+hipError_t reduce_mx4(const Mx4Problem &p, hipStream_t s) {
+  const size_t blocks = (static_cast<size_t>(p.M) * p.N / 4 + 255) / 256;
+  hipLaunchKernelGGL(k_mx4_reduce<OUT>, dim3(static_cast<unsigned>(std::min<size_t>(blocks, 65536))), dim3(256), 0,
+                     s, p);
+  return hipGetLastError();
+}
+
+template <class Cfg, int ACT, bool GROUPED>
+hipError_t run_tile16(const Mx4Problem &p, hipStream_t s) {
+  const int tn = (p.N + Cfg::BN - 1) / Cfg::BN;
+  const int tm = GROUPED ? p.M / Cfg::BM + std::min(p.E, p.M) : (p.M + Cfg::BM - 1) / Cfg::BM;
+  const int64_t grid = static_cast<int64_t>(tm) * tn * p.slices;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if constexpr (!GROUPED) {
+    if (p.slices > 1) {
+      hipLaunchKernelGGL((k_mx4_tile16<Cfg, ACT, false, true>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR),
+                         0, s, p, tm, tn);
+      return reduce_mx4<ACT>(p, s);
+    }
+  }
+  hipLaunchKernelGGL((k_mx4_tile16<Cfg, ACT, GROUPED, false>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0,
+                     s, p, tm, tn);
+  return hipGetLastError();
+}
+
+template <class Cfg, int OUT>
+hipError_t run_tile4(const Mx4Problem &p, hipStream_t s) {
+  const int tn = (p.N + Cfg::BN - 1) / Cfg::BN, tm = (p.M + Cfg::BM - 1) / Cfg::BM;
+  const int64_t grid = static_cast<int64_t>(tm) * tn * p.slices;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (p.slices > 1) {
+    hipLaunchKernelGGL((k_mx4_tile4<Cfg, OUT, true>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0, s, p,
+                       tm, tn);
+    return reduce_mx4<OUT>(p, s);
+  }
+  hipLaunchKernelGGL((k_mx4_tile4<Cfg, OUT, false>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0, s, p, tm,
+                     tn);
+  return hipGetLastError();
+}
+
+template <int ACT, bool GROUPED>
+hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
+  switch (tile) {
+    case kMx4L: return run_tile16<Cfg16L, ACT, GROUPED>(p, s);
+    case kMx4N: return run_tile16<Cfg16N, ACT, GROUPED>(p, s);
+    case kMx4M: return run_tile16<Cfg16M, ACT, GROUPED>(p, s);
+    case kMx4S: return run_tile16<Cfg16S, ACT, GROUPED>(p, s);
+    default: return run_stream<ACT, ACT, GROUPED>(p, s);
+  }
+}
+
+template <int OUT>
+hipError_t run_a4(const Mx4Problem &p, int tile, hipStream_t s) {
+  switch (tile) {
+    case kMx4L: return run_tile4<Cfg4L, OUT>(p, s);
+    case kMx4N: return run_tile4<Cfg4N, OUT>(p, s);
+    case kMx4M: return run_tile4<Cfg4M, OUT>(p, s);
+    case kMx4S: return run_tile4<Cfg4S, OUT>(p, s);
+    default: return run_stream<kMX4, OUT, false>(p, s);
+  }
+}
+
+}  // namespace
+
+size_t mx4_workspace_bytes(int m, int n, int k, int act_bits) {
+  return plan_mx4(m, n, k, act_bits == 4, false, 0).bytes;
+}
 
 hipError_t launch_mx4_gemm(const Mx4Args &a, hipStream_t s) {
-  const Mx4Problem p{a.A, reinterpret_cast<const uint32_t *>(a.AS), a.B,
-                     reinterpret_cast<const uint32_t *>(a.BS), a.bias, a.C, a.M, a.N, a.K, a.bias_dt,
-                     a.offsets, a.E};
+  Mx4Problem p{a.A, reinterpret_cast<const uint32_t *>(a.AS), a.B, reinterpret_cast<const uint32_t *>(a.BS),
+               a.bias, a.C, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, nullptr, 0, 1};
+  const Mx4Plan pl = plan_mx4(a.M, a.N, a.K, a.act == kMX4, a.offsets != nullptr, a.E);
+  if (pl.slices > 1 && a.ws && a.ws_bytes >= pl.bytes) {
+    p.part = static_cast<float *>(a.ws);
+    p.kseg = pl.kseg;
+    p.slices = pl.slices;
+  }
   if (a.act == kMX4) {
     switch (a.out) {
-      case QG_FP32: return run_stream<kMX4, QG_FP32, false>(p, s);
-      case QG_FP16: return run_stream<kMX4, QG_FP16, false>(p, s);
-      default: return run_stream<kMX4, QG_BF16, false>(p, s);
+      case QG_FP32: return run_a4<QG_FP32>(p, pl.tile, s);
+      case QG_FP16: return run_a4<QG_FP16>(p, pl.tile, s);
+      default: return run_a4<QG_BF16>(p, pl.tile, s);
     }
   }
   if (a.offsets)
-    return a.act == kFP16 ? run_stream<kFP16, QG_FP16, true>(p, s) : run_stream<kBF16, QG_BF16, true>(p, s);
-  return a.act == kFP16 ? run_stream<kFP16, QG_FP16, false>(p, s) : run_stream<kBF16, QG_BF16, false>(p, s);
+    return a.act == kFP16 ? run_a16<kFP16, true>(p, pl.tile, s) : run_a16<kBF16, true>(p, pl.tile, s);
+  return a.act == kFP16 ? run_a16<kFP16, false>(p, pl.tile, s) : run_a16<kBF16, false>(p, pl.tile, s);
 }
 
 }  // namespace qg

@@ -1,7 +1,8 @@
 // override.cpp -- the one dispatch override of libqgemm (qg_set_override in
 // include/qgemm.h): tests and tuning force the choices the host dispatch
 // otherwise makes from a problem's sizes (decode or prefill path, prefill
-// tile and split-K slices, MoE tile, W8A8 tile and slices).  The environment
+// tile and split-K slices, MoE tile, W8A8 tile and slices, MX4 kernel and
+// slices).  The environment
 // variable QGEMM_OVERRIDE gives the initial setting and is read once, on the
 // first dispatch; qg_set_override replaces the setting afterwards.  Nothing
 // else in the library reads the environment.
@@ -76,6 +77,15 @@ bool parse(const char *spec, Override &o) {
       o.w8a8_tile = t;
     } else if (k == "w8a8_split") {
       if (!parse_int(v, 1, 1024, o.w8a8_split)) return false;
+    } else if (k == "mx4_tile") {
+      static const char *names[] = {"stream", "T256", "T256N", "T128", "T64"};
+      int t = -1;
+      for (int i = 0; i < 5; ++i)
+        if (v == names[i]) t = i;
+      if (t < 0 && v != "auto") return false;
+      o.mx4_tile = t;
+    } else if (k == "mx4_split") {
+      if (!parse_int(v, 1, 1024, o.mx4_split)) return false;
     } else {
       return false;
     }

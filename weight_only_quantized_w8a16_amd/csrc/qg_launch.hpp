@@ -54,6 +54,9 @@ enum { kPathAuto = 0, kPathDecode = 1, kPathPrefill = 2 };
 enum PrefillTile { kX, kD8, kD8N, kD64, kD128, kL, kM, kS, kP256, kP128, kP64, kW256, kW256N, kW128, kW64, kWX, kDX };
 // W8A8 tiles (w8a8.hip), in the order qg_set_override names them.
 enum W8A8Tile { kT256, kT256N, kT128, kT64 };
+// MX4 kernels (mx4_gemm.hip), in the order qg_set_override names them: the
+// streaming kernel, then tiles of 256 x 256, 256 x 128, 128 x 128, 64 x 128.
+enum Mx4Kernel { kMx4Stream, kMx4L, kMx4N, kMx4M, kMx4S };
 struct Override {
   int path = kPathAuto;
   int prefill_tile = -1;       // PrefillTile, or -1
@@ -61,6 +64,8 @@ struct Override {
   bool moe_small_tile = false; // MoE grouped GEMMs on the 128 x 128 tile
   int w8a8_tile = -1;          // W8A8Tile, or -1
   int w8a8_split = 0;          // W8A8 K slices, or 0
+  int mx4_tile = -1;           // Mx4Kernel, or -1
+  int mx4_split = 0;           // MX4 K slices, or 0
 };
 Override dispatch_override();
 
