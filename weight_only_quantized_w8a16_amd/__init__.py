@@ -473,19 +473,23 @@ def _mx4_tiled_shapes(rows: int, k: int) -> tuple:
 
 
 def _mx4_multiple(func: str, k: int, step: int) -> None:
-    _need(k % step == 0, func, 7, f"k must be a multiple of {step} (got {k})")
+    if k % step:
+        raise QGemmError(func, 7, f"k must be a multiple of {step} (got {k})")
 
 
-def _mx4_devices(func: str, *named) -> int:
+def _mx4_devices(func: str, named) -> int:
     """The device index the given (tensor, name) pairs share; None is skipped."""
     dev = None
     for t, name in named:
         if t is None:
             continue
-        _dev(t, name)
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+            _dev(t, name)   # raises
+        d = t.get_device()
         if dev is None:
-            dev = t.get_device()
-        _need(t.get_device() == dev, func, _SHAPE, f"{name} must be on cuda:{dev} like the others")
+            dev = d
+        elif d != dev:
+            raise QGemmError(func, _SHAPE, f"{name} must be on cuda:{dev} like the others")
     return dev
 
 
@@ -493,31 +497,35 @@ def _mx4_call(func: str, dev: int, *args) -> None:
     """The library call, with the tensors' device as the current one."""
     fn = getattr(lib(), func)
     if dev == torch.cuda.current_device():
-        check(func, fn(*args))
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            check(func, fn(*args))
+            status = fn(*args)
+    if status:
+        check(func, status)
 
 
 def _check_mx4_pair(func: str, codes: torch.Tensor, scales: torch.Tensor, tiled: bool,
                     names=("codes", "scales"), lead: tuple = ()) -> tuple:
     """(rows held, k) of a codes / scales pair (after the leading dimensions)."""
-    nd = len(lead) + 2
+    cs = codes.shape
+    if codes.dtype == _U8 and scales.dtype == _U8 and len(cs) == len(lead) + 2 and cs[:-2] == lead:
+        rows, k = cs[-2], 2 * cs[-1]
+        if tiled:
+            want = lead + ((rows + 15) // 16, (k + 511) // 512, 64, 4)
+            if rows % 16 == 0 and k % 128 == 0 and scales.shape == want:
+                return rows, k
+            _need(rows % 16 == 0, func, 7, f"{names[0]} must hold whole 16-row tiles (got {rows} rows)")
+            _mx4_multiple(func, k, 128)
+        else:
+            want = lead + (rows, k // 32)
+            if k % 32 == 0 and scales.shape == want:
+                return rows, k
+            _mx4_multiple(func, k, 32)
+        _need(False, func, _SHAPE, f"{names[1]} must be {list(want)} (got {list(scales.shape)})")
     _need(codes.dtype == _U8 and scales.dtype == _U8, func, _DTYPE,
           f"{names[0]} and {names[1]} must be uint8")
-    _need(codes.dim() == nd and _shape(codes)[:-2] == lead, func, _SHAPE,
-          f"{names[0]} must be {list(lead)} + [rows, k/2] (got {list(codes.shape)})")
-    rows, k = codes.shape[-2], 2 * codes.shape[-1]
-    if tiled:
-        _need(rows % 16 == 0, func, 7, f"{names[0]} must hold whole 16-row tiles (got {rows} rows)")
-        _mx4_multiple(func, k, 128)
-        want = lead + _mx4_tiled_shapes(rows, k)[1]
-    else:
-        _mx4_multiple(func, k, 32)
-        want = lead + (rows, k // 32)
-    _need(_shape(scales) == want, func, _SHAPE,
-          f"{names[1]} must be {list(want)} (got {list(scales.shape)})")
-    return rows, k
+    _need(False, func, _SHAPE, f"{names[0]} must be {list(lead)} + [rows, k/2] (got {list(cs)})")
 
 
 def quantize_mx4(X: torch.Tensor, tiled: bool = False):
@@ -526,14 +534,15 @@ def quantize_mx4(X: torch.Tensor, tiled: bool = False):
     [rows, k/2] and [rows, k/32]) or, tiled, in the layout the products take
     (rows padded to 16; uint8 [R, k/2] and [R/16, ceil(k/512), 64, 4])."""
     f = "qquantize_mx4"
-    _need(X.dtype in _CODES and X.dim() >= 1, f, _DTYPE, f"X must be bf16, fp16 or fp32 (got {X.dtype})")
+    if X.dtype not in _CODES or X.dim() < 1:
+        raise QGemmError(f, _DTYPE, f"X must be bf16, fp16 or fp32 (got {X.dtype})")
     k = X.shape[-1]
     _mx4_multiple(f, k, 128 if tiled else 32)
-    dev = _mx4_devices(f, (X, "X"))
+    dev = _mx4_devices(f, ((X, "X"),))
     rows = X.numel() // k if k else 0
     shapes = _mx4_tiled_shapes(rows, k) if tiled else ((rows, k // 2), (rows, k // 32))
-    codes = torch.empty(shapes[0], dtype=_U8, device=X.device)
-    scales = torch.empty(shapes[1], dtype=_U8, device=X.device)
+    codes = X.new_empty(shapes[0], dtype=_U8)
+    scales = X.new_empty(shapes[1], dtype=_U8)
     _mx4_call(f, dev, _ptr(X), _ptr(codes), _ptr(scales), rows, k,
               QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[X.dtype], _stream(X))
     return codes, scales
@@ -544,12 +553,14 @@ def dequant_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtyp
     """MX4 codes and scales -> values [rows, k] in out_dtype.  rows: how many
     of the rows held are wanted (tiled matrices pad them to 16; default all)."""
     f = "qdequant_mx4"
-    _need(out_dtype in _CODES, f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
+    if out_dtype not in _CODES:
+        raise QGemmError(f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
     held, k = _check_mx4_pair(f, codes, scales, tiled)
     rows = held if rows is None else rows
-    _need(0 <= rows <= held, f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
-    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
-    out = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
+    if not 0 <= rows <= held:
+        raise QGemmError(f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
+    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
+    out = codes.new_empty((rows, k), dtype=out_dtype)
     _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(out), rows, k,
               QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[out_dtype], _stream(codes))
     return out
@@ -560,7 +571,7 @@ def repack_mx4(codes: torch.Tensor, scales: torch.Tensor):
     f = "qrepack_mx4"
     rows, k = _check_mx4_pair(f, codes, scales, False)
     _mx4_multiple(f, k, 128)
-    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
+    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
     shapes = _mx4_tiled_shapes(rows, k)
     tc = torch.empty(shapes[0], dtype=_U8, device=codes.device)
     ts = torch.empty(shapes[1], dtype=_U8, device=codes.device)
@@ -573,8 +584,9 @@ def unrepack_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: Optional[int] 
     f = "qunrepack_mx4"
     held, k = _check_mx4_pair(f, codes, scales, True)
     rows = held if rows is None else rows
-    _need(0 <= rows <= held, f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
-    dev = _mx4_devices(f, (codes, "codes"), (scales, "scales"))
+    if not 0 <= rows <= held:
+        raise QGemmError(f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
+    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
     pc = torch.empty((rows, k // 2), dtype=_U8, device=codes.device)
     ps = torch.empty((rows, k // 32), dtype=_U8, device=codes.device)
     _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(pc), _ptr(ps), rows, k, _stream(codes))
@@ -600,21 +612,23 @@ def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
     """C = A . value(B)^T (+ bias); A [..., k] bf16/fp16, B tiled MX4 [n, k]
     (repack_mx4, or quantize_mx4 with tiled=True)."""
     f = "qgemm_mx4a16"
-    _need(A.dtype in _ACT and A.dim() >= 1, f, _DTYPE, f"A must be bf16 or fp16 (got {A.dtype})")
+    if A.dtype not in _ACT or A.dim() < 1:
+        raise QGemmError(f, _DTYPE, f"A must be bf16 or fp16 (got {A.dtype})")
     n, k = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"))
-    _need(A.shape[-1] == k, f, _SHAPE, f"A must be [..., {k}] (got {list(A.shape)})")
+    if A.shape[-1] != k:
+        raise QGemmError(f, _SHAPE, f"A must be [..., {k}] (got {list(A.shape)})")
     _check_bias(f, bias, n)
     m = A.numel() // k if k else 0
     if out is not None:
         _check_out(f, out, A.dtype, m, n)
-    dev = _mx4_devices(f, (A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
-                       (out, "out"), (workspace, "workspace"))
-    C = out if out is not None else torch.empty((m, n), dtype=A.dtype, device=A.device)
+    dev = _mx4_devices(f, ((A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
+                           (out, "out"), (workspace, "workspace")))
+    C = out if out is not None else A.new_empty((*A.shape[:-1], n))
     ws, ws_bytes = _mx4_workspace(m, n, k, 16, A.device, workspace)
     _mx4_call(f, dev, _ptr(A), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C), m, n, k,
-              _CODES[A.dtype], dtype_code(None if bias is None else bias.dtype), _ptr(ws), ws_bytes,
+              _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype], _ptr(ws), ws_bytes,
               _stream(A))
-    return C.reshape(*A.shape[:-1], n)
+    return C if out is None else C.reshape(*A.shape[:-1], n)
 
 
 def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Tensor,
@@ -627,22 +641,26 @@ def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Ten
     f = "qgemm_mx4a4"
     held, k = _check_mx4_pair(f, A_tiled, A_scales, True, ("A_tiled", "A_scales"))
     n, kb = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"))
-    _need(k == kb, f, _SHAPE, f"A_tiled and B_tiled must have the same k (got {k} and {kb})")
+    if k != kb:
+        raise QGemmError(f, _SHAPE, f"A_tiled and B_tiled must have the same k (got {k} and {kb})")
     m = held if m is None else m
-    _need(0 <= m <= held, f, _SHAPE, f"m must be in [0, {held}] (got {m})")
+    if not 0 <= m <= held:
+        raise QGemmError(f, _SHAPE, f"m must be in [0, {held}] (got {m})")
     _check_bias(f, bias, n)
     if out is not None:
         out_dtype = out.dtype
         _check_out(f, out, out_dtype, m, n)
-    _need(out_dtype in _CODES, f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
-    dev = _mx4_devices(f, (A_tiled, "A_tiled"), (A_scales, "A_scales"), (B_tiled, "B_tiled"),
-                       (B_scales, "B_scales"), (bias, "bias"), (out, "out"), (workspace, "workspace"))
-    C = out if out is not None else torch.empty((m, n), dtype=out_dtype, device=A_tiled.device)
+    if out_dtype not in _CODES:
+        raise QGemmError(f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
+    dev = _mx4_devices(f, ((A_tiled, "A_tiled"), (A_scales, "A_scales"), (B_tiled, "B_tiled"),
+                           (B_scales, "B_scales"), (bias, "bias"), (out, "out"),
+                           (workspace, "workspace")))
+    C = out if out is not None else A_tiled.new_empty((m, n), dtype=out_dtype)
     ws, ws_bytes = _mx4_workspace(m, n, k, 4, A_tiled.device, workspace)
     _mx4_call(f, dev, _ptr(A_tiled), _ptr(A_scales), _ptr(B_tiled), _ptr(B_scales), _ptr(bias),
-              _ptr(C), m, n, k, _CODES[out_dtype], dtype_code(None if bias is None else bias.dtype),
+              _ptr(C), m, n, k, _CODES[out_dtype], QG_NONE if bias is None else _CODES[bias.dtype],
               _ptr(ws), ws_bytes, _stream(A_tiled))
-    return C
+    return C if out is None else C.reshape(m, n)
 
 
 def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.Tensor,
@@ -659,24 +677,26 @@ def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.T
     """
     f = "qgemm_mx4a16_grouped"
     _need(A.dtype in _ACT and A.dim() == 2, f, _DTYPE, "A must be a 2-D bf16 or fp16 tensor [rows, k]")
-    _need(offsets.dtype == torch.int32, f, _DTYPE, f"offsets must be int32 (got {offsets.dtype})")
+    if offsets.dtype != torch.int32:
+        raise QGemmError(f, _DTYPE, f"offsets must be int32 (got {offsets.dtype})")
     _need(offsets.dim() == 1 and offsets.numel() >= 2, f, _SHAPE, "offsets must be [E + 1], E >= 1")
     E = offsets.numel() - 1
     n, k = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"), lead=(E,))
     rows = A.shape[0]
-    _need(A.shape[1] == k, f, _SHAPE, f"A must be [rows, {k}] (got {list(A.shape)})")
+    if A.shape[1] != k:
+        raise QGemmError(f, _SHAPE, f"A must be [rows, {k}] (got {list(A.shape)})")
     if bias is not None:
         _need(bias.dtype in _ACT, f, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
         _need(_shape(bias) == (E, n), f, _SHAPE, f"bias must be [{E}, {n}] (got {list(bias.shape)})")
     if out is not None:
         _check_out(f, out, A.dtype, rows, n)
-    dev = _mx4_devices(f, (A, "A"), (offsets, "offsets"), (B_tiled, "B_tiled"),
-                       (B_scales, "B_scales"), (bias, "bias"), (out, "out"))
-    C = out if out is not None else torch.empty((rows, n), dtype=A.dtype, device=A.device)
+    dev = _mx4_devices(f, ((A, "A"), (offsets, "offsets"), (B_tiled, "B_tiled"),
+                           (B_scales, "B_scales"), (bias, "bias"), (out, "out")))
+    C = out if out is not None else A.new_empty((rows, n))
     _mx4_call(f, dev, _ptr(A), _ptr(offsets), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C),
-              rows, n, k, E, _CODES[A.dtype], dtype_code(None if bias is None else bias.dtype),
+              rows, n, k, E, _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype],
               _stream(A))
-    return C.reshape(rows, n)
+    return C if out is None else C.reshape(rows, n)
 
 
 # -- measurement probe -----------------------------------------------------------

@@ -42,15 +42,16 @@ __device__ __forceinline__ u32x4 mx4_word_to_operand(uint32_t w, float scale) {
 }
 
 // 16 x 16 x 128 product of two MX4 fragments (lane: row or column lane % 16,
-// block lane / 16 of the 128 k), each lane's block scale in byte 0 of its
+// block lane / 16 of the 128 k), each lane's block scale in byte B of its
 // scale word.
+template <int B>
 __device__ __forceinline__ f32x4 mx4_mfma(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb) {
   const i32x4 x = __builtin_bit_cast(i32x4, a), y = __builtin_bit_cast(i32x4, b);
   constexpr int kFP4 = 4;   // operand format code
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
       __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1),
-      __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1), c, kFP4, kFP4, 0,
-      static_cast<int>(sa), 0, static_cast<int>(sb));
+      __builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1), c, kFP4, kFP4, B,
+      static_cast<int>(sa), B, static_cast<int>(sb));
 }
 
 }  // namespace qg

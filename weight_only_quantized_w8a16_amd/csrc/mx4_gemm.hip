@@ -14,26 +14,11 @@
 #include <algorithm>
 
 #include "mx4_common.hpp"
-#include "mx4_tile16.hpp"
-#include "mx4_tile4.hpp"
+#include "mx4_tile.hpp"
 
 namespace qg {
 
 namespace {
-
-struct Mx4Problem {
-  const void *A;
-  const uint32_t *AS;
-  const uint8_t *B;
-  const uint32_t *BS;
-  const uint16_t *bias;
-  void *C;
-  int M, N, K, bias_dt;
-  const int32_t *offsets;
-  int E;
-  float *part;           // K slices: fp32 partial sums [slices, M, N], else null
-  int kseg, slices;      // 512-k windows per slice, slices
-};
 
 // Inclusive prefix sum over the wave.
 __device__ __forceinline__ int wave_scan(int x, int lane) {
@@ -73,17 +58,6 @@ __device__ __forceinline__ bool group_tile(const int32_t *offsets, int E, int M,
     before = __shfl(upto, 63);
   }
   return false;
-}
-
-// Row tiles of BM rows of a grouped product.
-__device__ __forceinline__ int group_tiles(const int32_t *offsets, int E, int M, int BM) {
-  const int lane = threadIdx.x & 63;
-  int cnt = 0;
-  for (int x = lane; x < E; x += 64) {
-    const int lo = min(max(offsets[x], 0), M), hi = max(min(max(offsets[x + 1], 0), M), lo);
-    cnt += (hi - lo + BM - 1) / BM;
-  }
-  return __shfl(wave_scan(cnt, lane), 63);
 }
 
 template <int OUT>
@@ -137,7 +111,7 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
           static_cast<const uint8_t *>(p.A) + (static_cast<size_t>(rt) * nb + kb) * 1024 + lane * 16);
       const uint32_t sa = p.AS[(static_cast<size_t>(rt) * nw + (kb >> 2)) * 64 + lane] >> (8 * (kb & 3));
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = mx4_mfma(w[i], a, acc[i], sw[i], sa);
+      for (int i = 0; i < NT; ++i) acc[i] = mx4_mfma<0>(w[i], a, acc[i], sw[i], sa);
     } else {
       const uint16_t *ap = static_cast<const uint16_t *>(p.A) + static_cast<size_t>(row) * K + kb * 128 + 32 * j;
       u32x4 a[4];
@@ -175,103 +149,125 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernels (mx4_tile16.hpp, mx4_tile4.hpp).
+// Tile kernels (mx4_tile.hpp).
 // ---------------------------------------------------------------------------
 
-// Workgroup b runs on XCD b % 8.  Of `count` working workgroups each XCD takes
-// a contiguous run of the tile order, so neighbouring tiles share an L2.
-__device__ __forceinline__ int xcd_order(int b, int count) {
-  const int xcd = b & 7, loc = b >> 3, per = count >> 3, rem = count & 7;
-  return (xcd < rem) ? xcd * (per + 1) + loc : rem * (per + 1) + (xcd - rem) * per + loc;
-}
-
-// Where a finished sum goes: C, rounded with its bias, or a K slice's partials.
-template <int OUT, bool SPLIT>
-struct Mx4Store {
-  const Mx4Problem &p;
-  const uint16_t *bias;   // of the tile's expert
-  int slice;
-  __device__ __forceinline__ void operator()(int r, int col, const float (&v)[4]) const {
-    if constexpr (SPLIT) {
-      float *P = p.part + static_cast<size_t>(slice) * p.M * p.N;
-      *reinterpret_cast<f32x4 *>(P + static_cast<size_t>(r) * p.N + col) = f32x4{v[0], v[1], v[2], v[3]};
+// Which items a workgroup walks.  Workgroup b runs on XCD b % 8; each XCD
+// takes a contiguous share of the item order, its workgroups neighbouring items at a
+// time, so that the XCD's L2 serves the rows and channels they share.
+struct Mx4Share {
+  int first, step, end;
+  __device__ __forceinline__ explicit Mx4Share(int total) {
+    const int b = blockIdx.x, grid = gridDim.x, xcd = b & 7, loc = b >> 3;
+    if (grid < 8) {
+      first = b; step = grid; end = total;
     } else {
-      float o[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = bias ? v[x] + bits_to_f32_dyn(bias[col + x], p.bias_dt) : v[x];
-      store4<OUT>(p.C, static_cast<size_t>(r) * p.N + col, o);
+      const int per = grid >> 3, rem = grid & 7;   // workgroups of this XCD: per, or one more
+      const int w0 = xcd * per + min(xcd, rem);
+      step = per + (xcd < rem ? 1 : 0);
+      first = static_cast<int>(static_cast<int64_t>(total) * w0 / grid) + loc;
+      end = static_cast<int>(static_cast<int64_t>(total) * (w0 + step) / grid);
     }
   }
 };
 
-// Row tile and column tile of this workgroup.  Dense: bands of four row tiles
-// walked column by column, so one weight tile serves the band's row tiles
-// while it is in L2.  Grouped: the column tiles of an expert's row tile next
-// to each other; the grid is sized for the most row tiles the offsets can
-// give, and workgroups past the real count end here.
-template <int BM, bool GROUPED>
-__device__ __forceinline__ bool mx4_tile_of(const Mx4Problem &p, int tiles_m, int tiles_n, int &tn, int &e,
-                                            int &slice, int &row0, int &row1) {
-  e = slice = 0;
-  if constexpr (GROUPED) {
-    const int count = group_tiles(p.offsets, p.E, p.M, BM) * tiles_n;
-    if (static_cast<int>(blockIdx.x) >= count) return false;
-    const int id = xcd_order(blockIdx.x, count), tm = id / tiles_n;
-    tn = id - tm * tiles_n;
-    return group_tile(p.offsets, p.E, p.M, BM, tm, e, row0, row1);
-  } else {
+// Dense: bands of four row tiles walked column by column, so one weight tile
+// serves the band's row tiles while it is in L2.
+template <class Eng>
+struct Mx4DenseWork {
+  const Mx4Problem &p;
+  const int tiles_m, tiles_n;
+  const Mx4Share share;
+  __device__ __forceinline__ explicit Mx4DenseWork(const Mx4Problem &pr)
+      : p(pr), tiles_m((pr.M + Eng::BM - 1) / Eng::BM), tiles_n((pr.N + Eng::BN - 1) / Eng::BN),
+        share(tiles_m * tiles_n * pr.slices) {}
+  __device__ __forceinline__ bool get(int n, Mx4Item &t) const {
+    int id = share.first + n * share.step;
+    if (id >= share.end) return false;
     constexpr int G = 4;
-    int id = xcd_order(blockIdx.x, gridDim.x);
     const int per = tiles_m * tiles_n;
-    slice = id / per;
-    id -= slice * per;
+    t.slice = id / per;
+    id -= t.slice * per;
     const int band = id / (G * tiles_n), first = band * G, gsz = min(G, tiles_m - first);
-    const int in = id - band * G * tiles_n;
-    tn = in / gsz;
-    row0 = (first + in % gsz) * BM;
-    row1 = min(p.M, row0 + BM);
+    const int in = id - band * G * tiles_n, tn = in / gsz;
+    t.row_lo = (first + in - tn * gsz) * Eng::BM;
+    t.row_last = min(p.M, t.row_lo + Eng::BM) - 1;
+    t.col_lo = tn * Eng::BN;
+    t.e = 0;
+    const int steps = p.K / Eng::K_STEP, seg = p.kseg * Eng::W;
+    t.s0 = p.slices > 1 ? t.slice * seg : 0;
+    t.s1 = p.slices > 1 ? min(steps, t.s0 + seg) : steps;
     return true;
   }
-}
+};
 
-template <class Cfg, int ACT, bool GROUPED, bool SPLIT>
-__global__ __launch_bounds__(Cfg::NTHR) void k_mx4_tile16(Mx4Problem p, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(16))) char a0[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char a1[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char a2[Cfg::NS > 2 ? Cfg::STAGE_A : 16];
-  __shared__ __attribute__((aligned(16))) char a3[Cfg::NS > 2 ? Cfg::STAGE_A : 16];
-  __shared__ __attribute__((aligned(16))) char b0[Cfg::STAGE_B];
-  __shared__ __attribute__((aligned(16))) char b1[Cfg::STAGE_B];
-  __shared__ __attribute__((aligned(16))) char b2[Cfg::NS > 2 ? Cfg::STAGE_B : 16];
-  __shared__ __attribute__((aligned(16))) char b3[Cfg::NS > 2 ? Cfg::STAGE_B : 16];
-  int tn, e, slice, row0, row1;
-  if (!mx4_tile_of<Cfg::BM, GROUPED>(p, tiles_m, tiles_n, tn, e, slice, row0, row1)) return;
-  const int nb = p.K >> 7, nw = mx4_scale_windows(p.K), ntiles = p.N >> 4, steps = p.K >> 6;
-  const Mx4Tile t{row0, row1 - 1, tn * Cfg::BN, SPLIT ? slice * p.kseg * 8 : 0,
-                  SPLIT ? min(steps, (slice + 1) * p.kseg * 8) : steps};
-  mx4_tile16<Cfg, ACT>(static_cast<const uint16_t *>(p.A), p.M, p.B + static_cast<size_t>(e) * ntiles * nb * 1024,
-                       p.BS + static_cast<size_t>(e) * ntiles * nw * 64, p.N, p.K, t,
-                       Mx4Lds{{a0, a1, a2, a3}, {b0, b1, b2, b3}},
-                       Mx4Store<ACT, SPLIT>{p, p.bias ? p.bias + static_cast<size_t>(e) * p.N : nullptr, slice});
-}
+// Grouped: the column tiles of an expert's row tile next to each other.  The
+// wave holds the row tiles of 64 experts at a time (a lane each); items come
+// in increasing order, so it moves on to the next 64 at most E / 64 times.
+template <class Eng>
+struct Mx4GroupWork {
+  const Mx4Problem &p;
+  const int tiles_n;
+  int e0, before, lo, hi, upto;   // before, upto: row tiles up to round e0 / the lane's expert
+  __device__ __forceinline__ int bound(int x) const { return min(max(p.offsets[x], 0), p.M); }
+  __device__ __forceinline__ void load(int start) {
+    const int x = start + (threadIdx.x & 63);
+    lo = hi = 0;
+    if (x < p.E) {
+      lo = bound(x);
+      hi = max(bound(x + 1), lo);
+    }
+    e0 = start;
+    upto = before + wave_scan((hi - lo + Eng::BM - 1) / Eng::BM, threadIdx.x & 63);
+  }
+  static __device__ __forceinline__ int total_tiles(const Mx4Problem &p) {
+    int cnt = 0;
+    for (int x = threadIdx.x & 63; x < p.E; x += 64) {
+      const int a = min(max(p.offsets[x], 0), p.M), b = max(min(max(p.offsets[x + 1], 0), p.M), a);
+      cnt += (b - a + Eng::BM - 1) / Eng::BM;
+    }
+    return __builtin_amdgcn_readlane(wave_scan(cnt, threadIdx.x & 63), 63);
+  }
+  const Mx4Share share;
+  __device__ __forceinline__ explicit Mx4GroupWork(const Mx4Problem &pr)
+      : p(pr), tiles_n((pr.N + Eng::BN - 1) / Eng::BN), before(0), share(total_tiles(pr) * tiles_n) {
+    load(0);
+  }
+  __device__ __forceinline__ bool get(int n, Mx4Item &t) {
+    const int id = share.first + n * share.step;
+    if (id >= share.end) return false;
+    const int tm = id / tiles_n;
+    int all = __builtin_amdgcn_readlane(upto, 63);
+    while (tm >= all) {
+      if (e0 + 64 >= p.E) return false;   // never: share counts the same tiles
+      before = all;
+      load(e0 + 64);
+      all = __builtin_amdgcn_readlane(upto, 63);
+    }
+    const int l = __builtin_ctzll(__ballot(tm < upto));
+    const int first = l == 0 ? before : __builtin_amdgcn_readlane(upto, l - 1);
+    t.e = e0 + l;
+    t.row_lo = __builtin_amdgcn_readlane(lo, l) + (tm - first) * Eng::BM;
+    t.row_last = min(__builtin_amdgcn_readlane(hi, l), t.row_lo + Eng::BM) - 1;
+    t.col_lo = (id - tm * tiles_n) * Eng::BN;
+    t.slice = t.s0 = 0;
+    t.s1 = p.K / Eng::K_STEP;
+    return true;
+  }
+};
 
-template <class Cfg, int OUT, bool SPLIT>
-__global__ __launch_bounds__(Cfg::NTHR) void k_mx4_tile4(Mx4Problem p, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(16))) char a0[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char a1[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char a2[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char a3[Cfg::STAGE_A];
-  __shared__ __attribute__((aligned(16))) char b0[Cfg::STAGE_B];
-  __shared__ __attribute__((aligned(16))) char b1[Cfg::STAGE_B];
-  __shared__ __attribute__((aligned(16))) char b2[Cfg::STAGE_B];
-  __shared__ __attribute__((aligned(16))) char b3[Cfg::STAGE_B];
-  int tn, e, slice, row0, row1;
-  if (!mx4_tile_of<Cfg::BM, false>(p, tiles_m, tiles_n, tn, e, slice, row0, row1)) return;
-  const int steps = p.K >> 7;
-  const Mx4Tile t{row0, row1 - 1, tn * Cfg::BN, SPLIT ? slice * p.kseg * 4 : 0,
-                  SPLIT ? min(steps, (slice + 1) * p.kseg * 4) : steps};
-  mx4_tile4<Cfg>(static_cast<const uint8_t *>(p.A), p.AS, p.M, p.B, p.BS, p.N, p.K, t,
-                 Mx4Lds{{a0, a1, a2, a3}, {b0, b1, b2, b3}}, Mx4Store<OUT, SPLIT>{p, p.bias, slice});
+template <class Eng, class Out, class Work>
+__global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem p) {
+  __shared__ __attribute__((aligned(16))) char s0[Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s1[Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 2 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s4[Eng::NS > 4 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s5[Eng::NS > 4 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s6[Eng::NS > 4 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s7[Eng::NS > 4 ? Eng::STAGE : 16];
+  Work work(p);
+  mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3, s4, s5, s6, s7}});
 }
 
 // K slices: C = RNE_out(the slices' partials summed in slice order + bias).
@@ -282,8 +278,10 @@ __global__ __launch_bounds__(256) void k_mx4_reduce(Mx4Problem p) {
     f32x4 s = *reinterpret_cast<const f32x4 *>(p.part + i);
     for (int sl = 1; sl < p.slices; ++sl) s += *reinterpret_cast<const f32x4 *>(p.part + sl * mn + i);
     const int r = static_cast<int>(i / p.N), col = static_cast<int>(i - static_cast<size_t>(r) * p.N);
-    const float v[4] = {s[0], s[1], s[2], s[3]};
-    Mx4Store<OUT, false>{p, p.bias, 0}(r, col, v);
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = p.bias ? s[x] + bits_to_f32_dyn(p.bias[col + x], p.bias_dt) : s[x];
+    store4<OUT>(p.C, i, v);
   }
 }
 
@@ -312,14 +310,24 @@ hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
 
 namespace {
 
-using Cfg16L = Mx4Cfg16<256, 256, 2, 4, 4>;   // waves of 128 x 64
-using Cfg16N = Mx4Cfg16<256, 128, 4, 2, 4>;   // waves of 64 x 64
-using Cfg16M = Mx4Cfg16<128, 128, 2, 4, 4>;   // waves of 64 x 32
-using Cfg16S = Mx4Cfg16<64, 128, 2, 4, 4>;    // waves of 32 x 32
-using Cfg4L = Mx4Cfg4<256, 256, 2, 4, 4>;     // waves of 128 x 64
-using Cfg4N = Mx4Cfg4<256, 128, 4, 2, 4>;     // waves of 64 x 64
-using Cfg4M = Mx4Cfg4<128, 128, 2, 4, 4>;     // waves of 64 x 32
-using Cfg4S = Mx4Cfg4<64, 128, 2, 4, 4>;      // waves of 32 x 32
+template <int T, int ACT> struct Tile16;
+template <int T> struct Tile4;
+template <int ACT> struct Tile16<1, ACT> { using Eng = Mx4Engine16<ACT, 256, 256, 2, 4, 4>; };
+template <int ACT> struct Tile16<2, ACT> { using Eng = Mx4Engine16<ACT, 128, 256, 2, 2, 2>; };
+template <int ACT> struct Tile16<3, ACT> { using Eng = Mx4Engine16<ACT, 128, 256, 2, 4, 4>; };
+template <int ACT> struct Tile16<4, ACT> { using Eng = Mx4Engine16<ACT, 128, 128, 2, 4, 4>; };
+template <int ACT> struct Tile16<5, ACT> { using Eng = Mx4Engine16<ACT, 128, 128, 2, 2, 4>; };
+template <int ACT> struct Tile16<6, ACT> { using Eng = Mx4Engine16<ACT, 64, 128, 2, 2, 8>; };
+template <int ACT> struct Tile16<7, ACT> { using Eng = Mx4Engine16<ACT, 64, 128, 2, 2, 4>; };
+template <int ACT> struct Tile16<8, ACT> { using Eng = Mx4Engine16<ACT, 64, 64, 2, 2, 8>; };
+template <> struct Tile4<1> { using Eng = Mx4Engine4<256, 256, 2, 4, 4>; };
+template <> struct Tile4<2> { using Eng = Mx4Engine4<128, 256, 2, 2, 2>; };
+template <> struct Tile4<3> { using Eng = Mx4Engine4<128, 256, 2, 4, 4>; };
+template <> struct Tile4<4> { using Eng = Mx4Engine4<128, 128, 2, 4, 4>; };
+template <> struct Tile4<5> { using Eng = Mx4Engine4<128, 128, 2, 2, 4>; };
+template <> struct Tile4<6> { using Eng = Mx4Engine4<64, 128, 2, 4, 4>; };
+template <> struct Tile4<7> { using Eng = Mx4Engine4<64, 128, 2, 2, 4>; };
+template <> struct Tile4<8> { using Eng = Mx4Engine4<64, 64, 2, 2, 4>; };
 
 struct Mx4Plan {
   int tile;            // Mx4Tile order below, or kStream
@@ -327,19 +335,17 @@ struct Mx4Plan {
   size_t bytes;        // partials
 };
 
-constexpr int tile_bm(int tile) { return tile == kMx4L || tile == kMx4N ? 256 : tile == kMx4M ? 128 : 64; }
-constexpr int tile_bn(int tile) { return tile == kMx4L ? 256 : 128; }
-
 Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   Mx4Plan pl{kMx4Stream, 0, 1, 0};
   const Override ov = dispatch_override();
   // 32-bit offsets of the tile kernels' buffer loads.
   const uint64_t lim = uint64_t(1) << 31;
   const uint64_t a_bytes = uint64_t((M + 15) / 16 * 16) * K / (a4 ? 2 : 1) * (a4 ? 1 : 2);
-  const bool fits = a_bytes < lim && uint64_t(N) * K / 2 < lim;
+  // A tile's rows of C (or of fp32 partials) in one buffer resource.
+  const bool fits = a_bytes < lim && uint64_t(N) * K / 2 < lim && uint64_t(N) * 4 * 256 < lim;
   if (!fits || ov.mx4_tile == kMx4Stream) return pl;
   if (ov.mx4_tile >= 0) pl.tile = ov.mx4_tile;
-  else if (M > 64) pl.tile = kMx4M;
+  else if (M > 64) pl.tile = 4;
   if (pl.tile == kMx4Stream) return pl;
   if (ov.mx4_split > 1 && !grouped) {
     const int windows = mx4_scale_windows(K), want = std::min(ov.mx4_split, windows);
@@ -358,46 +364,43 @@ hipError_t reduce_mx4(const Mx4Problem &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class Cfg, int ACT, bool GROUPED>
-hipError_t run_tile16(const Mx4Problem &p, hipStream_t s) {
-  const int tn = (p.N + Cfg::BN - 1) / Cfg::BN;
-  const int tm = GROUPED ? p.M / Cfg::BM + std::min(p.E, p.M) : (p.M + Cfg::BM - 1) / Cfg::BM;
-  const int64_t grid = static_cast<int64_t>(tm) * tn * p.slices;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  if constexpr (!GROUPED) {
-    if (p.slices > 1) {
-      hipLaunchKernelGGL((k_mx4_tile16<Cfg, ACT, false, true>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR),
-                         0, s, p, tm, tn);
-      return reduce_mx4<ACT>(p, s);
-    }
-  }
-  hipLaunchKernelGGL((k_mx4_tile16<Cfg, ACT, GROUPED, false>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0,
-                     s, p, tm, tn);
-  return hipGetLastError();
+// Workgroups of `Eng` a CU holds: by LDS, and by registers.
+template <class Eng>
+constexpr int groups_per_cu() {
+  const int lds = 160 * 1024 / (Eng::NS * Eng::STAGE), waves = 4 * Eng::WAVES / Eng::NW;
+  return std::max(1, std::min(lds, waves));
 }
 
-template <class Cfg, int OUT>
-hipError_t run_tile4(const Mx4Problem &p, hipStream_t s) {
-  const int tn = (p.N + Cfg::BN - 1) / Cfg::BN, tm = (p.M + Cfg::BM - 1) / Cfg::BM;
-  const int64_t grid = static_cast<int64_t>(tm) * tn * p.slices;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  if (p.slices > 1) {
-    hipLaunchKernelGGL((k_mx4_tile4<Cfg, OUT, true>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0, s, p,
-                       tm, tn);
+template <class Eng, int OUT, bool GROUPED>
+hipError_t run_tiles(const Mx4Problem &p, hipStream_t s) {
+  const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN;
+  // A grouped product has at most one partial row tile per expert with rows.
+  const int64_t tm = GROUPED ? p.M / Eng::BM + std::min(p.E, p.M) : (p.M + Eng::BM - 1) / Eng::BM;
+  const int64_t items = tm * tn * p.slices;
+  if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, device_cus() * groups_per_cu<Eng>()));
+  if constexpr (GROUPED) {
+    hipLaunchKernelGGL((k_mx4_tiles<Eng, Mx4Out<OUT, false>, Mx4GroupWork<Eng>>), dim3(grid), dim3(Eng::NTHR), 0, s, p);
+  } else if (p.slices > 1) {
+    hipLaunchKernelGGL((k_mx4_tiles<Eng, Mx4Out<OUT, true>, Mx4DenseWork<Eng>>), dim3(grid), dim3(Eng::NTHR), 0, s, p);
     return reduce_mx4<OUT>(p, s);
+  } else {
+    hipLaunchKernelGGL((k_mx4_tiles<Eng, Mx4Out<OUT, false>, Mx4DenseWork<Eng>>), dim3(grid), dim3(Eng::NTHR), 0, s, p);
   }
-  hipLaunchKernelGGL((k_mx4_tile4<Cfg, OUT, false>), dim3(static_cast<unsigned>(grid)), dim3(Cfg::NTHR), 0, s, p, tm,
-                     tn);
   return hipGetLastError();
 }
 
 template <int ACT, bool GROUPED>
 hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
   switch (tile) {
-    case kMx4L: return run_tile16<Cfg16L, ACT, GROUPED>(p, s);
-    case kMx4N: return run_tile16<Cfg16N, ACT, GROUPED>(p, s);
-    case kMx4M: return run_tile16<Cfg16M, ACT, GROUPED>(p, s);
-    case kMx4S: return run_tile16<Cfg16S, ACT, GROUPED>(p, s);
+    case 1: return run_tiles<typename Tile16<1, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 2: return run_tiles<typename Tile16<2, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 3: return run_tiles<typename Tile16<3, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 4: return run_tiles<typename Tile16<4, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 5: return run_tiles<typename Tile16<5, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 6: return run_tiles<typename Tile16<6, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 7: return run_tiles<typename Tile16<7, ACT>::Eng, ACT, GROUPED>(p, s);
+    case 8: return run_tiles<typename Tile16<8, ACT>::Eng, ACT, GROUPED>(p, s);
     default: return run_stream<ACT, ACT, GROUPED>(p, s);
   }
 }
@@ -405,10 +408,14 @@ hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
 template <int OUT>
 hipError_t run_a4(const Mx4Problem &p, int tile, hipStream_t s) {
   switch (tile) {
-    case kMx4L: return run_tile4<Cfg4L, OUT>(p, s);
-    case kMx4N: return run_tile4<Cfg4N, OUT>(p, s);
-    case kMx4M: return run_tile4<Cfg4M, OUT>(p, s);
-    case kMx4S: return run_tile4<Cfg4S, OUT>(p, s);
+    case 1: return run_tiles<Tile4<1>::Eng, OUT, false>(p, s);
+    case 2: return run_tiles<Tile4<2>::Eng, OUT, false>(p, s);
+    case 3: return run_tiles<Tile4<3>::Eng, OUT, false>(p, s);
+    case 4: return run_tiles<Tile4<4>::Eng, OUT, false>(p, s);
+    case 5: return run_tiles<Tile4<5>::Eng, OUT, false>(p, s);
+    case 6: return run_tiles<Tile4<6>::Eng, OUT, false>(p, s);
+    case 7: return run_tiles<Tile4<7>::Eng, OUT, false>(p, s);
+    case 8: return run_tiles<Tile4<8>::Eng, OUT, false>(p, s);
     default: return run_stream<kMX4, OUT, false>(p, s);
   }
 }
