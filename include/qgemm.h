@@ -97,7 +97,7 @@ int qg_version(void);
  *   moe_tile=auto|S                 S: the MoE on the 128 x 128 tile
  *   w8a8_tile=auto|T256|T256N|T128|T64   the W8A8 tile (also for m <= 16)
  *   w8a8_split=<n>                  W8A8 K slices, n >= 1
- *   mx4_tile=auto|stream|T256|T256N|T128|T64   the kernel of the MX4 products
+ *   mx4_tile=auto|stream|T256|T256N|T128|T64|T32   the kernel of the MX4 products
  *   mx4_split=<n>                   MX4 K slices, n >= 1
  * Keys not given take their automatic choice; NULL or "" restores every
  * automatic choice.  A forced choice that does not fit a problem (a

@@ -142,7 +142,7 @@ def test_conversions_leave_neighbours_alone():
 
 # m, n, k: one row to several row tiles, one column tile to several, odd counts
 # of both, every remainder of k modulo 512
-KERNELS = ["stream", "T1", "T2", "T3", "T4", "T5", "T6", "T7", "T8"]
+KERNELS = ["stream", "T256", "T256N", "T128", "T64", "T32"]
 SHAPES = [(1, 16, 128), (1, 2048, 2048), (2, 48, 256), (3, 80, 384), (16, 272, 640), (17, 96, 512),
           (31, 528, 896), (64, 144, 1152), (100, 400, 1024), (129, 656, 768), (300, 272, 1664)]
 

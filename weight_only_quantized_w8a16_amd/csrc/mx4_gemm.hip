@@ -73,10 +73,36 @@ __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4])
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Streaming kernel: a workgroup owns 16 rows and NT tiles of 16 columns, its
-// waves take 128-k blocks in turn, each lane the 16 bytes of one 32-value
-// block.  The waves' sums meet in LDS.
+// Streaming kernel, for few rows: a workgroup owns 16 rows and NT tiles of 16
+// columns, and its waves take 128-k blocks in turn, each lane the 16 bytes of
+// one 32-value block.  Nothing is shared between waves until their sums meet
+// in LDS, so no wave waits for another's loads.  Bound by HBM; row blocks of
+// 32 and 64 were slower than the tiles (every wave reads its activations out
+// of L2 by itself).
 // ---------------------------------------------------------------------------
+// 4 x 4 transpose over the four 16-lane rows of a wave: a[t] of lane row j and
+// a[j] of lane row t trade places.
+__device__ __forceinline__ void transpose_rows(u32x4 (&a)[4]) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const auto p = __builtin_amdgcn_permlane32_swap(a[0][d], a[2][d], false, false);
+    const auto q = __builtin_amdgcn_permlane32_swap(a[1][d], a[3][d], false, false);
+    const auto x = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
+    a[0][d] = x[0];
+    a[1][d] = x[1];
+    a[2][d] = y[0];
+    a[3][d] = y[1];
+  }
+}
+
+template <int ACT, int NT>
+struct Mx4StreamBlock {
+  static constexpr int AF = ACT == kMX4 ? 1 : 4;   // fragments of 16 rows and 128 k
+  u32x4 w[NT], a[AF];
+  uint32_t sw[NT], sa;
+};
+
 template <int ACT, int OUT, int NT, bool GROUPED>
 __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
   extern __shared__ __attribute__((aligned(16))) float red[];   // [wave][NT][64][4]
@@ -90,47 +116,83 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
   }
   const uint8_t *B = p.B + static_cast<size_t>(e) * ntiles * nb * 1024;
   const uint32_t *BS = p.BS + static_cast<size_t>(e) * ntiles * nw * 64;
-  const int row = min(row0 + nl, row1 - 1);   // rows past the end repeat the last; never stored
-
+  // Rows, row tiles and column tiles past the end repeat the last; their sums
+  // are not stored.
+  using Block = Mx4StreamBlock<ACT, NT>;
+  const uint8_t *wp[NT];
+  const uint32_t *sp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int nt = min(nt0 + i, ntiles - 1);
+    wp[i] = B + static_cast<size_t>(nt) * nb * 1024 + lane * 16;
+    sp[i] = BS + static_cast<size_t>(nt) * nw * 64 + lane;
+  }
+  const uint8_t *ap;
+  [[maybe_unused]] const uint32_t *asp = nullptr;
+  if constexpr (ACT == kMX4) {   // row0 is a multiple of 16 (not grouped)
+    ap = static_cast<const uint8_t *>(p.A) + static_cast<size_t>(row0 >> 4) * nb * 1024 + lane * 16;
+    asp = p.AS + static_cast<size_t>(row0 >> 4) * nw * 64 + lane;
+  } else {
+    const int row = min(row0 + nl, row1 - 1);
+    ap = static_cast<const uint8_t *>(p.A) + (static_cast<size_t>(row) * K + 8 * j) * 2;
+  }
+  auto load = [&](int kb, Block &f) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f.w[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + static_cast<size_t>(kb) * 1024));
+      f.sw[i] = sp[i][(kb >> 2) * 64];
+    }
+    if constexpr (ACT == kMX4) {
+      f.a[0] = *reinterpret_cast<const u32x4 *>(ap + static_cast<size_t>(kb) * 1024);
+      f.sa = asp[(kb >> 2) * 64];
+    } else {
+      // 64 contiguous bytes of each of 16 rows a load; the lanes trade them
+      // into the blocks' order below.
+#pragma unroll
+      for (int t = 0; t < 4; ++t) f.a[t] = *reinterpret_cast<const u32x4 *>(ap + static_cast<size_t>(kb) * 256 + 64 * t);
+    }
+  };
   f32x4 acc[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb = wave; kb < nb; kb += nwaves) {
-    u32x4 w[NT];
-    uint32_t sw[NT];
+  auto mma = [&](int kb, Block &f) {
+    const int sh = 8 * (kb & 3);
+    if constexpr (ACT != kMX4) transpose_rows(f.a);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int nt = min(nt0 + i, ntiles - 1);
-      w[i] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4 *>(B + (static_cast<size_t>(nt) * nb + kb) * 1024 + lane * 16));
-      sw[i] = BS[(static_cast<size_t>(nt) * nw + (kb >> 2)) * 64 + lane] >> (8 * (kb & 3));
-    }
-    if constexpr (ACT == kMX4) {
-      const int rt = row0 >> 4;   // row0 is a multiple of 16 (not grouped)
-      const u32x4 a = *reinterpret_cast<const u32x4 *>(
-          static_cast<const uint8_t *>(p.A) + (static_cast<size_t>(rt) * nb + kb) * 1024 + lane * 16);
-      const uint32_t sa = p.AS[(static_cast<size_t>(rt) * nw + (kb >> 2)) * 64 + lane] >> (8 * (kb & 3));
-#pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i] = mx4_mfma<0>(w[i], a, acc[i], sw[i], sa);
-    } else {
-      const uint16_t *ap = static_cast<const uint16_t *>(p.A) + static_cast<size_t>(row) * K + kb * 128 + 32 * j;
-      u32x4 a[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) a[t] = *reinterpret_cast<const u32x4 *>(ap + 8 * t);
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const float s = mx4_scale_operand(sw[i], 0);
+      if constexpr (ACT == kMX4) {
+        acc[i] = mx4_mfma<0>(f.w[i], f.a[0], acc[i], f.sw[i] >> sh, f.sa >> sh);
+      } else {
+        const float s = mx4_scale_operand(f.sw[i] >> sh, 0);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          acc[i] = mfma16x16x32<ACT>(mx4_word_to_operand<ACT>(w[i][t], s), a[t], acc[i]);
+          acc[i] = mfma16x16x32<ACT>(mx4_word_to_operand<ACT>(f.w[i][t], s), f.a[t], acc[i]);
       }
     }
+  };
+  // nwaves <= nb, so every wave has a block; past its last one a wave loads
+  // that one again (a branch around the loads would make every wait a full
+  // one).
+  Block f0, f1;
+  int kb = wave;
+  load(kb, f0);
+  for (;;) {
+    int next = kb + nwaves;
+    load(next < nb ? next : kb, f1);
+    mma(kb, f0);
+    if (next >= nb) break;
+    kb = next;
+    next += nwaves;
+    load(next < nb ? next : kb, f0);
+    mma(kb, f1);
+    if (next >= nb) break;
+    kb = next;
   }
+  // The waves' sums meet in LDS and are added in wave order; a thread finishes
+  // four consecutive columns, the quads of a tile on neighbouring threads.
 #pragma unroll
   for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(red + ((wave * NT + i) * 64 + lane) * 4) = acc[i];
   __syncthreads();
-  // Thread (row r, tile i, column quad c): four consecutive columns, the quads
-  // of a tile on neighbouring threads.
   for (int q = threadIdx.x; q < NT * 64; q += blockDim.x) {
     const int c = q & 3, i = (q >> 2) % NT, r = q / (4 * NT);
     if (row0 + r >= row1 || nt0 + i >= ntiles) continue;
@@ -262,12 +324,22 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem 
   __shared__ __attribute__((aligned(16))) char s1[Eng::STAGE];
   __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? Eng::STAGE : 16];
   __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 2 ? Eng::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char s4[Eng::NS > 4 ? Eng::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char s5[Eng::NS > 4 ? Eng::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char s6[Eng::NS > 4 ? Eng::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char s7[Eng::NS > 4 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char ep[Out::kBytes == 2 ? Eng::EP : 16];
+  __shared__ __attribute__((aligned(16))) float bias[Eng::NW * Eng::WTN];
   Work work(p);
-  mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3, s4, s5, s6, s7}});
+  mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3}, ep, bias});
+}
+
+template <class Eng, int KW, class Out, class Work>
+__global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
+  __shared__ __attribute__((aligned(16))) float bias[Eng::NW * Eng::WTN];
+  __shared__ __attribute__((aligned(16))) char s0[KW * Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s1[KW * Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? KW * Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 3 ? KW * Eng::STAGE : 16];
+  Work work(p);
+  Mx4Item t;
+  if (work.get(0, t)) mx4_one_tile<Eng, KW, Out>(p, t, Mx4Lds{{s0, s1, s2, s3}, nullptr, bias});
 }
 
 // K slices: C = RNE_out(the slices' partials summed in slice order + bias).
@@ -289,15 +361,11 @@ namespace {
 
 constexpr int kMaxSlabs = 65535;   // grid.y
 
-template <int ACT, int OUT, bool GROUPED>
-hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
-  constexpr int NT = 2;
+template <int ACT, int OUT, int NT, bool GROUPED>
+hipError_t run_stream_as(const Mx4Problem &p, long slabs, hipStream_t s) {
   const int nb = p.K >> 7, waves = nb < 8 ? nb : 8;
   const size_t lds = static_cast<size_t>(waves) * NT * 256 * sizeof(float);
   const unsigned cols = static_cast<unsigned>(((p.N >> 4) + NT - 1) / NT);
-  // Row slabs: a grouped product has at most one partial slab per expert
-  // with rows.
-  const long slabs = GROUPED ? p.M / 16 + std::min(p.E, p.M) : (static_cast<long>(p.M) + 15) / 16;
   for (long s0 = 0; s0 < slabs; s0 += kMaxSlabs) {
     const unsigned ny = static_cast<unsigned>(std::min<long>(slabs - s0, kMaxSlabs));
     hipLaunchKernelGGL((k_mx4_stream<ACT, OUT, NT, GROUPED>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
@@ -306,53 +374,124 @@ hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Column tiles a workgroup: one while there are few (each workgroup a CU's
+// share), two or four when there are many, so that a workgroup's activations,
+// its start and its final sum serve more weight bytes.  Measured at M = 1:
+// N = 2048 3.8 us with one, 4.0 with two; N = 18944 (K = 3584) 12.7 with one,
+// 10.6 with two, 11.1 with four; N = 131072 45, 25.9 and 24.7.  With more rows
+// the activations weigh more: M = 13, N = 18944 14.5 with two, 13.6 with four.
+template <int ACT, int OUT, bool GROUPED>
+hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
+  // Row slabs: a grouped product has at most one partial slab per expert
+  // with rows.
+  const long slabs = GROUPED ? p.M / 16 + std::min(p.E, p.M) : (p.M + 15) / 16;
+  const long tiles = (p.N >> 4) * slabs;
+  if (tiles < 512) return run_stream_as<ACT, OUT, 1, GROUPED>(p, slabs, s);
+  if (tiles < 1024 || (tiles < 4096 && (p.M <= 4 || ACT == kMX4))) return run_stream_as<ACT, OUT, 2, GROUPED>(p, slabs, s);
+  return run_stream_as<ACT, OUT, 4, GROUPED>(p, slabs, s);
+}
+
 }  // namespace
 
 namespace {
 
-template <int T, int ACT> struct Tile16;
-template <int T> struct Tile4;
-template <int ACT> struct Tile16<1, ACT> { using Eng = Mx4Engine16<ACT, 256, 256, 2, 4, 4>; };
-template <int ACT> struct Tile16<2, ACT> { using Eng = Mx4Engine16<ACT, 128, 256, 2, 2, 2>; };
-template <int ACT> struct Tile16<3, ACT> { using Eng = Mx4Engine16<ACT, 128, 256, 2, 4, 4>; };
-template <int ACT> struct Tile16<4, ACT> { using Eng = Mx4Engine16<ACT, 128, 128, 2, 4, 4>; };
-template <int ACT> struct Tile16<5, ACT> { using Eng = Mx4Engine16<ACT, 128, 128, 2, 2, 4>; };
-template <int ACT> struct Tile16<6, ACT> { using Eng = Mx4Engine16<ACT, 64, 128, 2, 2, 8>; };
-template <int ACT> struct Tile16<7, ACT> { using Eng = Mx4Engine16<ACT, 64, 128, 2, 2, 4>; };
-template <int ACT> struct Tile16<8, ACT> { using Eng = Mx4Engine16<ACT, 64, 64, 2, 2, 8>; };
-template <> struct Tile4<1> { using Eng = Mx4Engine4<256, 256, 2, 4, 4>; };
-template <> struct Tile4<2> { using Eng = Mx4Engine4<128, 256, 2, 2, 2>; };
-template <> struct Tile4<3> { using Eng = Mx4Engine4<128, 256, 2, 4, 4>; };
-template <> struct Tile4<4> { using Eng = Mx4Engine4<128, 128, 2, 4, 4>; };
-template <> struct Tile4<5> { using Eng = Mx4Engine4<128, 128, 2, 2, 4>; };
-template <> struct Tile4<6> { using Eng = Mx4Engine4<64, 128, 2, 4, 4>; };
-template <> struct Tile4<7> { using Eng = Mx4Engine4<64, 128, 2, 2, 4>; };
-template <> struct Tile4<8> { using Eng = Mx4Engine4<64, 64, 2, 2, 4>; };
+// The tiles.  T256 .. T64 walk their tiles in a fixed set of workgroups; T32
+// runs one tile a workgroup, k dealt out to KW groups of waves.
+template <int TILE, int ACT> struct Mx4Tiling;
+template <int ACT> struct Mx4Tiling<kMx4T256, ACT> { using Eng = Mx4Engine16<ACT, 256, 256, 2, 4, 2, false>; };
+template <int ACT> struct Mx4Tiling<kMx4T256N, ACT> { using Eng = Mx4Engine16<ACT, 128, 256, 2, 4, 4, true>; };
+template <int ACT> struct Mx4Tiling<kMx4T128, ACT> { using Eng = Mx4Engine16<ACT, 128, 128, 2, 2, 2, false>; };
+template <int ACT> struct Mx4Tiling<kMx4T64, ACT> { using Eng = Mx4Engine16<ACT, 64, 128, 2, 2, 4, true>; };
+template <int ACT> struct Mx4Tiling<kMx4T32, ACT> { using Eng = Mx4Engine16<ACT, 32, 64, 1, 2, 3, false>; };
+template <> struct Mx4Tiling<kMx4T256, kMX4> { using Eng = Mx4Engine4<256, 256, 2, 4, 4>; };
+template <> struct Mx4Tiling<kMx4T256N, kMX4> { using Eng = Mx4Engine4<128, 256, 2, 4, 4>; };
+template <> struct Mx4Tiling<kMx4T128, kMX4> { using Eng = Mx4Engine4<128, 128, 2, 2, 4>; };
+template <> struct Mx4Tiling<kMx4T64, kMX4> { using Eng = Mx4Engine4<64, 128, 2, 2, 4>; };
+template <> struct Mx4Tiling<kMx4T32, kMX4> { using Eng = Mx4Engine4<32, 64, 1, 2, 3>; };
+constexpr int kT32Groups = 4;
+
+// What a tile costs, in microseconds: a launch (t0), and per 64 k
+// lone + shared * q with q workgroups a CU running at a time, at most `most`
+// (lone: a workgroup's chain of steps; shared: what the workgroups take from
+// each other).  Fitted on MI355X to 128, 256 and 512 workgroups at k = 2048
+// and 6144.
+struct Mx4Cost {
+  int bm, bn, most;
+  float t0, lone, shared;
+};
+constexpr Mx4Cost kCost16[] = {{256, 256, 1, 12.f, 0.81f, 0.72f}, {128, 256, 1, 5.f, 0.43f, 0.52f},
+                               {128, 128, 2, 4.f, 0.48f, 0.25f}, {64, 128, 2, 4.f, 0.15f, 0.28f},
+                               {32, 64, 2, 3.5f, 0.06f, 0.09f}};
+constexpr Mx4Cost kCost4[] = {{256, 256, 1, 7.f, 0.295f, 0.354f}, {128, 256, 1, 6.f, 0.29f, 0.09f},
+                              {128, 128, 2, 5.f, 0.165f, 0.11f}, {64, 128, 2, 4.5f, 0.14f, 0.08f},
+                              {32, 64, 2, 4.5f, 0.06f, 0.0375f}};
 
 struct Mx4Plan {
-  int tile;            // Mx4Tile order below, or kStream
+  int tile;            // Mx4Kernel
   int kseg, slices;    // K slices in 512-k windows
   size_t bytes;        // partials
 };
 
+// Time of `tiles` tiles of `steps` 64-k steps each: full rounds of the
+// workgroups the CUs hold, and what is left.
+float tiles_time(const Mx4Cost &c, float tiles, float steps) {
+  const float q = tiles / static_cast<float>(device_cus()), most = static_cast<float>(c.most);
+  const float rounds = static_cast<float>(static_cast<int>(q / most)), rest = q - rounds * most;
+  return c.t0 + steps * (rounds * (c.lone + c.shared * most) + (rest > 0.f ? c.lone + c.shared * rest : 0.f));
+}
+
+// The tile, and for few tiles the K slices, with the least time by the
+// measured costs; a slice's partials cost another launch and their traffic.
+// Up to 16 rows the streaming kernel, which reads each weight once with no
+// row padding beyond 16 (m = 13, n = 18944, k = 3584: 13.6 us against 15.0 on
+// 32 x 64 tiles; m = 32: 20.4 against 16.8).  A grouped product's row tiles
+// are not known to the host: it reckons with half a tile too many for every
+// expert, and streams up to a mean of 12 rows an expert (64 experts, n = 2816,
+// k = 2048: 512 rows 45.7 us against 49.9 on 64 x 128 tiles, 1024 rows 62.9
+// against 58.8).
 Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   Mx4Plan pl{kMx4Stream, 0, 1, 0};
   const Override ov = dispatch_override();
-  // 32-bit offsets of the tile kernels' buffer loads.
+  // 32-bit offsets of the tile kernels' buffer loads and stores: the operands,
+  // and a tile's rows of C (or of fp32 partials).
   const uint64_t lim = uint64_t(1) << 31;
   const uint64_t a_bytes = uint64_t((M + 15) / 16 * 16) * K / (a4 ? 2 : 1) * (a4 ? 1 : 2);
-  // A tile's rows of C (or of fp32 partials) in one buffer resource.
-  const bool fits = a_bytes < lim && uint64_t(N) * K / 2 < lim && uint64_t(N) * 4 * 256 < lim;
-  if (!fits || ov.mx4_tile == kMx4Stream) return pl;
-  if (ov.mx4_tile >= 0) pl.tile = ov.mx4_tile;
-  else if (M > 64) pl.tile = 4;
-  if (pl.tile == kMx4Stream) return pl;
-  if (ov.mx4_split > 1 && !grouped) {
-    const int windows = mx4_scale_windows(K), want = std::min(ov.mx4_split, windows);
+  if (a_bytes >= lim || uint64_t(N) * K / 2 >= lim || uint64_t(N) * 4 * 256 >= lim) return pl;
+  const Mx4Cost *cost = a4 ? kCost4 : kCost16;
+  const int windows = mx4_scale_windows(K);
+  if (ov.mx4_tile >= 0) {
+    pl.tile = ov.mx4_tile;
+  } else if (grouped ? M > 12 * static_cast<int64_t>(E) : M > 16) {
+    float best = 0.f;
+    for (int i = 0; i < 5; ++i) {
+      const int64_t cols = (N + cost[i].bn - 1) / cost[i].bn;
+      const float tiles = static_cast<float>(cols) *
+                          (grouped ? static_cast<float>(M) / cost[i].bm + 0.5f * E
+                                   : static_cast<float>((M + cost[i].bm - 1) / cost[i].bm));
+      for (int s = 1; s <= 8 && (s == 1 || (!grouped && s <= windows / 2)); ++s) {
+        const int kseg = (windows + s - 1) / s;
+        if ((windows + kseg - 1) / kseg != s) continue;
+        float t = tiles_time(cost[i], tiles * s, s == 1 ? K / 64.f : kseg * 8.f);
+        if (s > 1) t += 3.f + static_cast<float>(s + 1) * M * N * 4.f / 3.5e6f;
+        if (best == 0.f || t < best) {
+          best = t;
+          pl.tile = kMx4T256 + i;
+          pl.slices = s;
+          pl.kseg = kseg;
+        }
+      }
+    }
+  }
+  if (pl.tile == kMx4Stream || grouped) {
+    pl.slices = 1;
+    return pl;
+  }
+  if (ov.mx4_split > 0) {
+    const int want = std::min(ov.mx4_split, windows);
     pl.kseg = (windows + want - 1) / want;
     pl.slices = (windows + pl.kseg - 1) / pl.kseg;
-    if (pl.slices > 1) pl.bytes = static_cast<size_t>(pl.slices) * M * N * sizeof(float);
   }
+  if (pl.slices > 1) pl.bytes = static_cast<size_t>(pl.slices) * M * N * sizeof(float);
   return pl;
 }
 
@@ -367,7 +506,7 @@ hipError_t reduce_mx4(const Mx4Problem &p, hipStream_t s) {
 // Workgroups of `Eng` a CU holds: by LDS, and by registers.
 template <class Eng>
 constexpr int groups_per_cu() {
-  const int lds = 160 * 1024 / (Eng::NS * Eng::STAGE), waves = 4 * Eng::WAVES / Eng::NW;
+  const int lds = 160 * 1024 / (Eng::NS * Eng::STAGE + Eng::EP), waves = 4 * Eng::WAVES / Eng::NW;
   return std::max(1, std::min(lds, waves));
 }
 
@@ -390,17 +529,32 @@ hipError_t run_tiles(const Mx4Problem &p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class Eng, int KW, int OUT, bool GROUPED>
+hipError_t run_one_tile(const Mx4Problem &p, hipStream_t s) {
+  const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN;
+  const int64_t tm = GROUPED ? p.M / Eng::BM + std::min(p.E, p.M) : (p.M + Eng::BM - 1) / Eng::BM;
+  const int64_t items = tm * tn * p.slices;
+  if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(items)), block(Eng::NTHR * KW);
+  if constexpr (GROUPED) {
+    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, false>, Mx4GroupWork<Eng>>), grid, block, 0, s, p);
+  } else if (p.slices > 1) {
+    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, true>, Mx4DenseWork<Eng>>), grid, block, 0, s, p);
+    return reduce_mx4<OUT>(p, s);
+  } else {
+    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, false>, Mx4DenseWork<Eng>>), grid, block, 0, s, p);
+  }
+  return hipGetLastError();
+}
+
 template <int ACT, bool GROUPED>
 hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
   switch (tile) {
-    case 1: return run_tiles<typename Tile16<1, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 2: return run_tiles<typename Tile16<2, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 3: return run_tiles<typename Tile16<3, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 4: return run_tiles<typename Tile16<4, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 5: return run_tiles<typename Tile16<5, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 6: return run_tiles<typename Tile16<6, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 7: return run_tiles<typename Tile16<7, ACT>::Eng, ACT, GROUPED>(p, s);
-    case 8: return run_tiles<typename Tile16<8, ACT>::Eng, ACT, GROUPED>(p, s);
+    case kMx4T256: return run_tiles<typename Mx4Tiling<kMx4T256, ACT>::Eng, ACT, GROUPED>(p, s);
+    case kMx4T256N: return run_tiles<typename Mx4Tiling<kMx4T256N, ACT>::Eng, ACT, GROUPED>(p, s);
+    case kMx4T128: return run_tiles<typename Mx4Tiling<kMx4T128, ACT>::Eng, ACT, GROUPED>(p, s);
+    case kMx4T64: return run_tiles<typename Mx4Tiling<kMx4T64, ACT>::Eng, ACT, GROUPED>(p, s);
+    case kMx4T32: return run_one_tile<typename Mx4Tiling<kMx4T32, ACT>::Eng, kT32Groups, ACT, GROUPED>(p, s);
     default: return run_stream<ACT, ACT, GROUPED>(p, s);
   }
 }
@@ -408,14 +562,11 @@ hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
 template <int OUT>
 hipError_t run_a4(const Mx4Problem &p, int tile, hipStream_t s) {
   switch (tile) {
-    case 1: return run_tiles<Tile4<1>::Eng, OUT, false>(p, s);
-    case 2: return run_tiles<Tile4<2>::Eng, OUT, false>(p, s);
-    case 3: return run_tiles<Tile4<3>::Eng, OUT, false>(p, s);
-    case 4: return run_tiles<Tile4<4>::Eng, OUT, false>(p, s);
-    case 5: return run_tiles<Tile4<5>::Eng, OUT, false>(p, s);
-    case 6: return run_tiles<Tile4<6>::Eng, OUT, false>(p, s);
-    case 7: return run_tiles<Tile4<7>::Eng, OUT, false>(p, s);
-    case 8: return run_tiles<Tile4<8>::Eng, OUT, false>(p, s);
+    case kMx4T256: return run_tiles<Mx4Tiling<kMx4T256, kMX4>::Eng, OUT, false>(p, s);
+    case kMx4T256N: return run_tiles<Mx4Tiling<kMx4T256N, kMX4>::Eng, OUT, false>(p, s);
+    case kMx4T128: return run_tiles<Mx4Tiling<kMx4T128, kMX4>::Eng, OUT, false>(p, s);
+    case kMx4T64: return run_tiles<Mx4Tiling<kMx4T64, kMX4>::Eng, OUT, false>(p, s);
+    case kMx4T32: return run_one_tile<Mx4Tiling<kMx4T32, kMX4>::Eng, kT32Groups, OUT, false>(p, s);
     default: return run_stream<kMX4, OUT, false>(p, s);
   }
 }

@@ -78,9 +78,9 @@ bool parse(const char *spec, Override &o) {
     } else if (k == "w8a8_split") {
       if (!parse_int(v, 1, 1024, o.w8a8_split)) return false;
     } else if (k == "mx4_tile") {
-      static const char *names[] = {"stream", "T1", "T2", "T3", "T4", "T5", "T6", "T7", "T8"};
+      static const char *names[] = {"stream", "T256", "T256N", "T128", "T64", "T32"};
       int t = -1;
-      for (int i = 0; i < 9; ++i)
+      for (int i = 0; i < 6; ++i)
         if (v == names[i]) t = i;
       if (t < 0 && v != "auto") return false;
       o.mx4_tile = t;

@@ -55,8 +55,9 @@ enum PrefillTile { kX, kD8, kD8N, kD64, kD128, kL, kM, kS, kP256, kP128, kP64, k
 // W8A8 tiles (w8a8.hip), in the order qg_set_override names them.
 enum W8A8Tile { kT256, kT256N, kT128, kT64 };
 // MX4 kernels (mx4_gemm.hip), in the order qg_set_override names them: the
-// streaming kernel, then tiles of 256 x 256, 256 x 128, 128 x 128, 64 x 128.
-enum Mx4Kernel { kMx4Stream, kMx4L, kMx4N, kMx4M, kMx4S };
+// streaming kernel, then tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and
+// 32 x 64.
+enum Mx4Kernel { kMx4Stream, kMx4T256, kMx4T256N, kMx4T128, kMx4T64, kMx4T32 };
 struct Override {
   int path = kPathAuto;
   int prefill_tile = -1;       // PrefillTile, or -1
