@@ -478,7 +478,15 @@ def _mx4_multiple(func: str, k: int, step: int) -> None:
 
 
 def _mx4_devices(func: str, named) -> int:
-    """The device index the given (tensor, name) pairs share; None is skipped."""
+    """The device index the given (tensor, name) pairs share; None is skipped.
+    Raises for tensors off the device, on another one, or not contiguous."""
+    dev = named[0][0].get_device()
+    for t, _ in named:
+        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
+            break
+    else:
+        if dev >= 0:
+            return dev
     dev = None
     for t, name in named:
         if t is None:
@@ -493,10 +501,18 @@ def _mx4_devices(func: str, named) -> int:
     return dev
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _mx4_stream(dev: int):
+    """Raw handle of torch's current stream on device dev."""
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _mx4_call(func: str, dev: int, *args) -> None:
     """The library call, with the tensors' device as the current one."""
     fn = getattr(lib(), func)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -543,8 +559,8 @@ def quantize_mx4(X: torch.Tensor, tiled: bool = False):
     shapes = _mx4_tiled_shapes(rows, k) if tiled else ((rows, k // 2), (rows, k // 32))
     codes = X.new_empty(shapes[0], dtype=_U8)
     scales = X.new_empty(shapes[1], dtype=_U8)
-    _mx4_call(f, dev, _ptr(X), _ptr(codes), _ptr(scales), rows, k,
-              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[X.dtype], _stream(X))
+    _mx4_call(f, dev, X.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, k,
+              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[X.dtype], _mx4_stream(dev))
     return codes, scales
 
 
@@ -561,8 +577,8 @@ def dequant_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtyp
         raise QGemmError(f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
     dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
     out = codes.new_empty((rows, k), dtype=out_dtype)
-    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(out), rows, k,
-              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[out_dtype], _stream(codes))
+    _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), rows, k,
+              QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[out_dtype], _mx4_stream(dev))
     return out
 
 
@@ -575,7 +591,7 @@ def repack_mx4(codes: torch.Tensor, scales: torch.Tensor):
     shapes = _mx4_tiled_shapes(rows, k)
     tc = torch.empty(shapes[0], dtype=_U8, device=codes.device)
     ts = torch.empty(shapes[1], dtype=_U8, device=codes.device)
-    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(tc), _ptr(ts), rows, k, _stream(codes))
+    _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), tc.data_ptr(), ts.data_ptr(), rows, k, _mx4_stream(dev))
     return tc, ts
 
 
@@ -589,7 +605,7 @@ def unrepack_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: Optional[int] 
     dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
     pc = torch.empty((rows, k // 2), dtype=_U8, device=codes.device)
     ps = torch.empty((rows, k // 32), dtype=_U8, device=codes.device)
-    _mx4_call(f, dev, _ptr(codes), _ptr(scales), _ptr(pc), _ptr(ps), rows, k, _stream(codes))
+    _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), pc.data_ptr(), ps.data_ptr(), rows, k, _mx4_stream(dev))
     return pc, ps
 
 
@@ -597,13 +613,17 @@ def mx4_workspace_size(m: int, n: int, k: int, act_bits: int) -> int:
     return int(lib().qgemm_mx4_workspace_size(m, n, k, act_bits))
 
 
-def _mx4_workspace(m: int, n: int, k: int, act_bits: int, device, given: Optional[torch.Tensor]):
+def _mx4_workspace(m: int, n: int, k: int, act_bits: int, like: torch.Tensor,
+                   given: Optional[torch.Tensor]):
+    """(tensor, address, bytes) of workspace: the caller's, else a fresh one
+    when the library asks for any."""
     if given is not None:
-        return given, given.numel() * given.element_size()
-    need = mx4_workspace_size(m, n, k, act_bits)
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    need = lib().qgemm_mx4_workspace_size(m, n, k, act_bits)
     if need == 0:
-        return None, 0
-    return torch.empty(need, dtype=_U8, device=device), need
+        return None, None, 0
+    ws = like.new_empty((need,), dtype=_U8)
+    return ws, ws.data_ptr(), need
 
 
 def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
@@ -624,10 +644,10 @@ def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
     dev = _mx4_devices(f, ((A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
                            (out, "out"), (workspace, "workspace")))
     C = out if out is not None else A.new_empty((*A.shape[:-1], n))
-    ws, ws_bytes = _mx4_workspace(m, n, k, 16, A.device, workspace)
-    _mx4_call(f, dev, _ptr(A), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C), m, n, k,
-              _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype], _ptr(ws), ws_bytes,
-              _stream(A))
+    ws, ws_ptr, ws_bytes = _mx4_workspace(m, n, k, 16, A, workspace)
+    _mx4_call(f, dev, A.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias), C.data_ptr(), m, n, k,
+              _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype], ws_ptr, ws_bytes,
+              _mx4_stream(dev))
     return C if out is None else C.reshape(*A.shape[:-1], n)
 
 
@@ -656,10 +676,10 @@ def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Ten
                            (B_scales, "B_scales"), (bias, "bias"), (out, "out"),
                            (workspace, "workspace")))
     C = out if out is not None else A_tiled.new_empty((m, n), dtype=out_dtype)
-    ws, ws_bytes = _mx4_workspace(m, n, k, 4, A_tiled.device, workspace)
-    _mx4_call(f, dev, _ptr(A_tiled), _ptr(A_scales), _ptr(B_tiled), _ptr(B_scales), _ptr(bias),
-              _ptr(C), m, n, k, _CODES[out_dtype], QG_NONE if bias is None else _CODES[bias.dtype],
-              _ptr(ws), ws_bytes, _stream(A_tiled))
+    ws, ws_ptr, ws_bytes = _mx4_workspace(m, n, k, 4, A_tiled, workspace)
+    _mx4_call(f, dev, A_tiled.data_ptr(), A_scales.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias),
+              C.data_ptr(), m, n, k, _CODES[out_dtype], QG_NONE if bias is None else _CODES[bias.dtype],
+              ws_ptr, ws_bytes, _mx4_stream(dev))
     return C if out is None else C.reshape(m, n)
 
 
@@ -693,9 +713,9 @@ def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.T
     dev = _mx4_devices(f, ((A, "A"), (offsets, "offsets"), (B_tiled, "B_tiled"),
                            (B_scales, "B_scales"), (bias, "bias"), (out, "out")))
     C = out if out is not None else A.new_empty((rows, n))
-    _mx4_call(f, dev, _ptr(A), _ptr(offsets), _ptr(B_tiled), _ptr(B_scales), _ptr(bias), _ptr(C),
+    _mx4_call(f, dev, A.data_ptr(), offsets.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias), C.data_ptr(),
               rows, n, k, E, _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype],
-              _stream(A))
+              _mx4_stream(dev))
     return C if out is None else C.reshape(rows, n)
 
 

@@ -410,21 +410,29 @@ template <> struct Mx4Tiling<kMx4T64, kMX4> { using Eng = Mx4Engine4<64, 128, 2,
 template <> struct Mx4Tiling<kMx4T32, kMX4> { using Eng = Mx4Engine4<32, 64, 1, 2, 3>; };
 constexpr int kT32Groups = 4;
 
-// What a tile costs, in microseconds: a launch (t0), and per 64 k
-// lone + shared * q with q workgroups a CU running at a time, at most `most`
-// (lone: a workgroup's chain of steps; shared: what the workgroups take from
-// each other).  Fitted on MI355X to 128, 256 and 512 workgroups at k = 2048
-// and 6144.
+// What a tile costs, in microseconds: a launch (t0), and per 64 k `full` while
+// a CU runs as many workgroups as it does at a time (most), lone + shared * q
+// with a mean of q < most (lone: a workgroup's chain of steps; shared: what
+// the workgroups take from each other).  Fitted to 2868 timings on MI355X, 17
+// to 4096 rows and eight weight shapes of 512 x 2048 to 18944 x 3584, each
+// tile and slice count forced (residual 6 to 8 %); the tile it picks is within
+// 3 % of the best one on average, 29 % at worst.
 struct Mx4Cost {
   int bm, bn, most;
-  float t0, lone, shared;
+  float t0, lone, shared, full;
 };
-constexpr Mx4Cost kCost16[] = {{256, 256, 1, 12.f, 0.81f, 0.72f}, {128, 256, 1, 5.f, 0.43f, 0.52f},
-                               {128, 128, 2, 4.f, 0.48f, 0.25f}, {64, 128, 2, 4.f, 0.15f, 0.28f},
-                               {32, 64, 2, 3.5f, 0.06f, 0.09f}};
-constexpr Mx4Cost kCost4[] = {{256, 256, 1, 7.f, 0.295f, 0.354f}, {128, 256, 1, 6.f, 0.29f, 0.09f},
-                              {128, 128, 2, 5.f, 0.165f, 0.11f}, {64, 128, 2, 4.5f, 0.14f, 0.08f},
-                              {32, 64, 2, 4.5f, 0.06f, 0.0375f}};
+constexpr Mx4Cost kCost16[] = {{256, 256, 1, 10.9f, 0.988f, 0.303f, 1.534f},
+                               {128, 256, 1, 7.3f, 0.550f, 0.173f, 0.819f},
+                               {128, 128, 2, 4.8f, 0.394f, 0.221f, 0.880f},
+                               {64, 128, 2, 5.5f, 0.228f, 0.120f, 0.505f},
+                               {32, 64, 2, 5.5f, 0.045f, 0.069f, 0.200f}};
+constexpr Mx4Cost kCost4[] = {{256, 256, 1, 10.2f, 0.336f, 0.077f, 0.504f},
+                              {128, 256, 1, 6.8f, 0.218f, 0.077f, 0.302f},
+                              {128, 128, 2, 6.0f, 0.140f, 0.073f, 0.319f},
+                              {64, 128, 2, 5.1f, 0.105f, 0.048f, 0.207f},
+                              {32, 64, 2, 5.6f, 0.029f, 0.037f, 0.123f}};
+// K slices: the reduction's launch, and a byte of partials (in the same fit).
+constexpr float kSliceLaunch = 2.3f, kSliceByte = 2.8e-7f;
 
 struct Mx4Plan {
   int tile;            // Mx4Kernel
@@ -437,7 +445,7 @@ struct Mx4Plan {
 float tiles_time(const Mx4Cost &c, float tiles, float steps) {
   const float q = tiles / static_cast<float>(device_cus()), most = static_cast<float>(c.most);
   const float rounds = static_cast<float>(static_cast<int>(q / most)), rest = q - rounds * most;
-  return c.t0 + steps * (rounds * (c.lone + c.shared * most) + (rest > 0.f ? c.lone + c.shared * rest : 0.f));
+  return c.t0 + steps * (rounds * c.full + (rest > 0.f ? c.lone + c.shared * rest : 0.f));
 }
 
 // The tile, and for few tiles the K slices, with the least time by the
@@ -446,8 +454,9 @@ float tiles_time(const Mx4Cost &c, float tiles, float steps) {
 // row padding beyond 16 (m = 13, n = 18944, k = 3584: 13.6 us against 15.0 on
 // 32 x 64 tiles; m = 32: 20.4 against 16.8).  A grouped product's row tiles
 // are not known to the host: it reckons with half a tile too many for every
-// expert, and streams up to a mean of 12 rows an expert (64 experts, n = 2816,
-// k = 2048: 512 rows 45.7 us against 49.9 on 64 x 128 tiles, 1024 rows 62.9
+// expert, takes no 32-row tiles (2048 rows over 64 experts, n = 2816, k = 2048:
+// 85.6 us against 64.6 on 64-row ones), and streams up to a mean of 12 rows an
+// expert (512 rows: 45.7 us against 49.9 on 64-row tiles, 1024 rows 62.9
 // against 58.8).
 Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   Mx4Plan pl{kMx4Stream, 0, 1, 0};
@@ -463,16 +472,16 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
     pl.tile = ov.mx4_tile;
   } else if (grouped ? M > 12 * static_cast<int64_t>(E) : M > 16) {
     float best = 0.f;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < (grouped ? 4 : 5); ++i) {
       const int64_t cols = (N + cost[i].bn - 1) / cost[i].bn;
       const float tiles = static_cast<float>(cols) *
                           (grouped ? static_cast<float>(M) / cost[i].bm + 0.5f * E
                                    : static_cast<float>((M + cost[i].bm - 1) / cost[i].bm));
-      for (int s = 1; s <= 8 && (s == 1 || (!grouped && s <= windows / 2)); ++s) {
+      for (int s = 1; s <= 4 && (s == 1 || (!grouped && s <= windows / 2)); ++s) {
         const int kseg = (windows + s - 1) / s;
         if ((windows + kseg - 1) / kseg != s) continue;
         float t = tiles_time(cost[i], tiles * s, s == 1 ? K / 64.f : kseg * 8.f);
-        if (s > 1) t += 3.f + static_cast<float>(s + 1) * M * N * 4.f / 3.5e6f;
+        if (s > 1) t += kSliceLaunch + static_cast<float>(s + 1) * M * N * 4.f * kSliceByte;
         if (best == 0.f || t < best) {
           best = t;
           pl.tile = kMx4T256 + i;
