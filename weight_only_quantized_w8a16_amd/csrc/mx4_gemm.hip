@@ -103,7 +103,7 @@ struct Mx4StreamBlock {
   uint32_t sw[NT], sa;
 };
 
-template <int ACT, int OUT, int NT, bool GROUPED>
+template <int ACT, int OUT, int NT, bool GROUPED, int DEPTH>
 __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
   extern __shared__ __attribute__((aligned(16))) float red[];   // [wave][NT][64][4]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
@@ -170,23 +170,18 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
       }
     }
   };
-  // nwaves <= nb, so every wave has a block; past its last one a wave loads
-  // that one again (a branch around the loads would make every wait a full
-  // one).
-  Block f0, f1;
-  int kb = wave;
-  load(kb, f0);
-  for (;;) {
-    int next = kb + nwaves;
-    load(next < nb ? next : kb, f1);
-    mma(kb, f0);
-    if (next >= nb) break;
-    kb = next;
-    next += nwaves;
-    load(next < nb ? next : kb, f0);
-    mma(kb, f1);
-    if (next >= nb) break;
-    kb = next;
+  // DEPTH blocks at a time, all of their loads on the way before the first is
+  // waited for.  nwaves <= nb, so every wave has a block; past its last one a
+  // wave loads that one again (a branch around the loads would make every
+  // wait a full one) and skips the product.
+  Block f[DEPTH];
+  for (int kb = wave; kb < nb; kb += DEPTH * nwaves) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(kb + d * nwaves < nb ? kb + d * nwaves : kb, f[d]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (kb + d * nwaves < nb) mma(kb + d * nwaves, f[d]);
   }
   // The waves' sums meet in LDS and are added in wave order; a thread finishes
   // four consecutive columns, the quads of a tile on neighbouring threads.
@@ -361,34 +356,36 @@ namespace {
 
 constexpr int kMaxSlabs = 65535;   // grid.y
 
-template <int ACT, int OUT, int NT, bool GROUPED>
+template <int ACT, int OUT, int NT, bool GROUPED, int DEPTH>
 hipError_t run_stream_as(const Mx4Problem &p, long slabs, hipStream_t s) {
   const int nb = p.K >> 7, waves = nb < 8 ? nb : 8;
   const size_t lds = static_cast<size_t>(waves) * NT * 256 * sizeof(float);
   const unsigned cols = static_cast<unsigned>(((p.N >> 4) + NT - 1) / NT);
   for (long s0 = 0; s0 < slabs; s0 += kMaxSlabs) {
     const unsigned ny = static_cast<unsigned>(std::min<long>(slabs - s0, kMaxSlabs));
-    hipLaunchKernelGGL((k_mx4_stream<ACT, OUT, NT, GROUPED>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
+    hipLaunchKernelGGL((k_mx4_stream<ACT, OUT, NT, GROUPED, DEPTH>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
                        static_cast<int>(s0));
   }
   return hipGetLastError();
 }
-
 // Column tiles a workgroup: one while there are few (each workgroup a CU's
-// share), two or four when there are many, so that a workgroup's activations,
-// its start and its final sum serve more weight bytes.  Measured at M = 1:
-// N = 2048 3.8 us with one, 4.0 with two; N = 18944 (K = 3584) 12.7 with one,
-// 10.6 with two, 11.1 with four; N = 131072 45, 25.9 and 24.7.  With more rows
-// the activations weigh more: M = 13, N = 18944 14.5 with two, 13.6 with four.
+// share; two blocks' loads in flight a wave), two or four when there are many,
+// so that a workgroup's activations, its start and its final sum serve more
+// weight bytes.  Measured at M = 1: N = 2048 3.6 us with one, 4.1 with two;
+// N = 18944 (K = 3584) 12.5 with one, 10.8 with two or four; N = 131072 38,
+// 26.7 and 24.2 (5.9 TB/s of weights); M = 13, N = 18944 17.8, 13.2 and 12.9.
+// MX4 activations weigh less: M = 8, N = 18944 9.2 with two, 10.4 with four.
+// Depth two with one tile: N = 3584, K = 3584 5.0 -> 4.6 us, MX4 activations
+// at K = 18944 14.3 -> 11.7; with more tiles it gains nothing.
 template <int ACT, int OUT, bool GROUPED>
 hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
   // Row slabs: a grouped product has at most one partial slab per expert
   // with rows.
   const long slabs = GROUPED ? p.M / 16 + std::min(p.E, p.M) : (p.M + 15) / 16;
   const long tiles = (p.N >> 4) * slabs;
-  if (tiles < 512) return run_stream_as<ACT, OUT, 1, GROUPED>(p, slabs, s);
-  if (tiles < 1024 || (tiles < 4096 && (p.M <= 4 || ACT == kMX4))) return run_stream_as<ACT, OUT, 2, GROUPED>(p, slabs, s);
-  return run_stream_as<ACT, OUT, 4, GROUPED>(p, slabs, s);
+  if (tiles < 512) return run_stream_as<ACT, OUT, 1, GROUPED, 2>(p, slabs, s);
+  if (tiles < 1024 || (tiles < 4096 && ACT == kMX4)) return run_stream_as<ACT, OUT, 2, GROUPED, 1>(p, slabs, s);
+  return run_stream_as<ACT, OUT, 4, GROUPED, 1>(p, slabs, s);
 }
 
 }  // namespace

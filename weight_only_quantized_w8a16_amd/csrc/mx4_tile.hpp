@@ -739,8 +739,8 @@ __device__ __forceinline__ void mx4_tiles(const Mx4Problem &p, Work &work, const
 template <class Eng, int KW, class Out>
 __device__ __forceinline__ void mx4_one_tile(const Mx4Problem &p, const Mx4Item &t, const Mx4Lds &L) {
   constexpr int NS = Eng::NS, LOADS = Eng::LOADS + Eng::STEP_SCALE_LOADS;
-  constexpr int PER = KW * Eng::STAGE / (Eng::NW * Eng::PART);   // groups' sums a stage holds
-  static_assert((KW == 1 || KW - 1 <= PER * NS) && Eng::EP <= KW * Eng::STAGE, "LDS reuse");
+  constexpr int PER = KW * Eng::STAGE / Eng::PART;   // waves' sums a stage holds
+  static_assert((KW - 1) * Eng::NW <= PER * NS && Eng::EP <= KW * Eng::STAGE, "LDS reuse");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = wave / Eng::NW;
   Eng eng(p, wave % Eng::NW);
   typename Eng::StepScales sc[NS];
@@ -775,14 +775,18 @@ __device__ __forceinline__ void mx4_one_tile(const Mx4Problem &p, const Mx4Item 
   __builtin_amdgcn_s_waitcnt(mx4_wait(0));
   __syncthreads();   // every group is done with the stages
   if constexpr (KW > 1) {
-    const int mine = wave % Eng::NW * Eng::PART;
+    // Wave w of group x + 1 at unit x * NW + w of the stages.
+    const int w = wave % Eng::NW;
+    auto at_unit = [&](int u, auto &&use) {
 #pragma unroll
-    for (int x = 0; x < KW - 1; ++x)
-      if (g == x + 1) eng.put_part(L.s[x / PER] + x % PER * Eng::NW * Eng::PART + mine);
+      for (int q = 0; q < NS; ++q)
+        if (u / PER == q) use(L.s[q] + u % PER * Eng::PART);
+    };
+    if (g > 0) at_unit((g - 1) * Eng::NW + w, [&](char *part) { eng.put_part(part); });
     __syncthreads();
     if (g == 0) {
 #pragma unroll
-      for (int x = 0; x < KW - 1; ++x) eng.add_part(L.s[x / PER] + x % PER * Eng::NW * Eng::PART + mine);
+      for (int x = 0; x < KW - 1; ++x) at_unit(x * Eng::NW + w, [&](const char *part) { eng.add_part(part); });
     }
     __syncthreads();
     if (g > 0) return;
