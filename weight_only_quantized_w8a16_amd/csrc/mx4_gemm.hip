@@ -20,7 +20,7 @@ namespace qg {
 
 namespace {
 
-// Inclusive prefix sum over the wave.
+// Inclusive prefix sum and maximum over the wave.
 __device__ __forceinline__ int wave_scan(int x, int lane) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -29,36 +29,56 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
   }
   return x;
 }
-
-// Row tile `id` of a grouped product: expert e and its rows [row0, row1), at
-// most BM of them; false past the last tile.  Offsets are clamped to
-// [0, M] and a decrease counts as no rows, so no offset leads outside.
-__device__ __forceinline__ bool group_tile(const int32_t *offsets, int E, int M, int BM, int id, int &e,
-                                           int &row0, int &row1) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;   // tiles of the experts of earlier rounds
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int x = e0 + lane;
-    int lo = 0, hi = 0;
-    if (x < E) {
-      lo = min(max(offsets[x], 0), M);
-      hi = max(min(max(offsets[x + 1], 0), M), lo);
-    }
-    const int cnt = (hi - lo + BM - 1) / BM;
-    const int upto = before + wave_scan(cnt, lane);
-    const unsigned long long mine = __ballot(id < upto);
-    if (mine) {
-      const int l = __builtin_ctzll(mine);
-      const int first = __shfl(upto - cnt, l);
-      e = e0 + l;
-      row0 = __shfl(lo, l) + (id - first) * BM;
-      row1 = min(__shfl(hi, l), row0 + BM);
-      return true;
-    }
-    before = __shfl(upto, 63);
+__device__ __forceinline__ int wave_scan_max(int x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(x, off);
+    if (lane >= off) x = max(x, y);
   }
-  return false;
+  return x;
 }
+
+// The row tiles of a grouped product, 64 experts at a time, one a lane.
+// Offsets are clamped to [0, M] and never go back: expert e's rows run from
+// the largest offset up to e to the largest up to e + 1.  So whatever the
+// offsets hold, no row lies outside, none belongs to two experts, and there
+// are at most M / BM + min(E, M) row tiles, which is what the grids assume.
+struct Mx4Groups {
+  const int32_t *offsets;
+  int E, M, BM;
+  int e0, lo, hi;      // the lane's expert is e0 + lane; its rows [lo, hi)
+  int before, upto;    // row tiles before expert e0, and up to the lane's
+  __device__ __forceinline__ int bound(int x) const { return min(max(offsets[x], 0), M); }
+  __device__ __forceinline__ void load(int start, int from, int tiles) {   // from: the largest offset up to start
+    const int lane = threadIdx.x & 63, x = start + lane;
+    hi = max(wave_scan_max(x < E ? bound(x + 1) : 0, lane), from);
+    lo = __shfl_up(hi, 1);
+    if (lane == 0) lo = from;
+    e0 = start;
+    before = tiles;
+    upto = tiles + wave_scan((hi - lo + BM - 1) / BM, lane);
+  }
+  __device__ __forceinline__ Mx4Groups(const Mx4Problem &p, int bm) : offsets(p.offsets), E(p.E), M(p.M), BM(bm) {
+    load(0, bound(0), 0);
+  }
+  __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(upto, 63); }   // up to e0 + 63
+  __device__ __forceinline__ bool more() const { return e0 + 64 < E; }
+  __device__ __forceinline__ void next() { load(e0 + 64, __builtin_amdgcn_readlane(hi, 63), tiles()); }
+  // Row tile id, at or after the current 64 experts: expert e, rows
+  // [row0, row1); false past the last.
+  __device__ __forceinline__ bool find(int id, int &e, int &row0, int &row1) {
+    while (id >= tiles()) {
+      if (!more()) return false;
+      next();
+    }
+    const int l = __builtin_ctzll(__ballot(id < upto));
+    const int first = l == 0 ? before : __builtin_amdgcn_readlane(upto, l - 1);
+    e = e0 + l;
+    row0 = __builtin_amdgcn_readlane(lo, l) + (id - first) * BM;
+    row1 = min(__builtin_amdgcn_readlane(hi, l), row0 + BM);
+    return true;
+  }
+};
 
 template <int OUT>
 __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4]) {
@@ -112,7 +132,8 @@ __global__ __launch_bounds__(512) void k_mx4_stream(Mx4Problem p, int slab0) {
   const int nt0 = blockIdx.x * NT;
   int row0 = (slab0 + static_cast<int>(blockIdx.y)) * 16, row1 = min(p.M, row0 + 16), e = 0;
   if constexpr (GROUPED) {
-    if (!group_tile(p.offsets, p.E, p.M, 16, slab0 + blockIdx.y, e, row0, row1)) return;
+    Mx4Groups groups(p, 16);
+    if (!groups.find(slab0 + blockIdx.y, e, row0, row1)) return;
   }
   const uint8_t *B = p.B + static_cast<size_t>(e) * ntiles * nb * 1024;
   const uint32_t *BS = p.BS + static_cast<size_t>(e) * ntiles * nw * 64;
@@ -258,57 +279,32 @@ struct Mx4DenseWork {
   }
 };
 
-// Grouped: the column tiles of an expert's row tile next to each other.  The
-// wave holds the row tiles of 64 experts at a time (a lane each); items come
-// in increasing order, so it moves on to the next 64 at most E / 64 times.
+// Grouped: the column tiles of an expert's row tile next to each other.  Items
+// come in increasing order, so the wave moves on to the next 64 experts at
+// most E / 64 times.
 template <class Eng>
 struct Mx4GroupWork {
-  const Mx4Problem &p;
-  const int tiles_n;
-  int e0, before, lo, hi, upto;   // before, upto: row tiles up to round e0 / the lane's expert
-  __device__ __forceinline__ int bound(int x) const { return min(max(p.offsets[x], 0), p.M); }
-  __device__ __forceinline__ void load(int start) {
-    const int x = start + (threadIdx.x & 63);
-    lo = hi = 0;
-    if (x < p.E) {
-      lo = bound(x);
-      hi = max(bound(x + 1), lo);
-    }
-    e0 = start;
-    upto = before + wave_scan((hi - lo + Eng::BM - 1) / Eng::BM, threadIdx.x & 63);
-  }
-  static __device__ __forceinline__ int total_tiles(const Mx4Problem &p) {
-    int cnt = 0;
-    for (int x = threadIdx.x & 63; x < p.E; x += 64) {
-      const int a = min(max(p.offsets[x], 0), p.M), b = max(min(max(p.offsets[x + 1], 0), p.M), a);
-      cnt += (b - a + Eng::BM - 1) / Eng::BM;
-    }
-    return __builtin_amdgcn_readlane(wave_scan(cnt, threadIdx.x & 63), 63);
-  }
+  const int tiles_n, steps;
+  Mx4Groups groups;
   const Mx4Share share;
-  __device__ __forceinline__ explicit Mx4GroupWork(const Mx4Problem &pr)
-      : p(pr), tiles_n((pr.N + Eng::BN - 1) / Eng::BN), before(0), share(total_tiles(pr) * tiles_n) {
-    load(0);
+  static __device__ __forceinline__ int total(const Mx4Problem &p) {
+    Mx4Groups g(p, Eng::BM);
+    while (g.more()) g.next();
+    return g.tiles();
   }
+  __device__ __forceinline__ explicit Mx4GroupWork(const Mx4Problem &p)
+      : tiles_n((p.N + Eng::BN - 1) / Eng::BN), steps(p.K / Eng::K_STEP), groups(p, Eng::BM),
+        share(total(p) * tiles_n) {}
   __device__ __forceinline__ bool get(int n, Mx4Item &t) {
     const int id = share.first + n * share.step;
     if (id >= share.end) return false;
     const int tm = id / tiles_n;
-    int all = __builtin_amdgcn_readlane(upto, 63);
-    while (tm >= all) {
-      if (e0 + 64 >= p.E) return false;   // never: share counts the same tiles
-      before = all;
-      load(e0 + 64);
-      all = __builtin_amdgcn_readlane(upto, 63);
-    }
-    const int l = __builtin_ctzll(__ballot(tm < upto));
-    const int first = l == 0 ? before : __builtin_amdgcn_readlane(upto, l - 1);
-    t.e = e0 + l;
-    t.row_lo = __builtin_amdgcn_readlane(lo, l) + (tm - first) * Eng::BM;
-    t.row_last = min(__builtin_amdgcn_readlane(hi, l), t.row_lo + Eng::BM) - 1;
+    int row1;
+    if (!groups.find(tm, t.e, t.row_lo, row1)) return false;
+    t.row_last = row1 - 1;
     t.col_lo = (id - tm * tiles_n) * Eng::BN;
     t.slice = t.s0 = 0;
-    t.s1 = p.K / Eng::K_STEP;
+    t.s1 = steps;
     return true;
   }
 };
@@ -325,14 +321,14 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem 
   mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3}, ep, bias});
 }
 
-template <class Eng, int KW, class Out, class Work>
+template <class Eng, int KW, class Out>
 __global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
   __shared__ __attribute__((aligned(16))) float bias[Eng::NW * Eng::WTN];
   __shared__ __attribute__((aligned(16))) char s0[KW * Eng::STAGE];
   __shared__ __attribute__((aligned(16))) char s1[KW * Eng::STAGE];
   __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? KW * Eng::STAGE : 16];
   __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 3 ? KW * Eng::STAGE : 16];
-  Work work(p);
+  const Mx4DenseWork<Eng> work(p);
   Mx4Item t;
   if (work.get(0, t)) mx4_one_tile<Eng, KW, Out>(p, t, Mx4Lds{{s0, s1, s2, s3}, nullptr, bias});
 }
@@ -465,7 +461,7 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   if (a_bytes >= lim || uint64_t(N) * K / 2 >= lim || uint64_t(N) * 4 * 256 >= lim) return pl;
   const Mx4Cost *cost = a4 ? kCost4 : kCost16;
   const int windows = mx4_scale_windows(K);
-  if (ov.mx4_tile >= 0) {
+  if (ov.mx4_tile >= 0 && !(grouped && ov.mx4_tile == kMx4T32)) {
     pl.tile = ov.mx4_tile;
   } else if (grouped ? M > 12 * static_cast<int64_t>(E) : M > 16) {
     float best = 0.f;
@@ -535,21 +531,17 @@ hipError_t run_tiles(const Mx4Problem &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class Eng, int KW, int OUT, bool GROUPED>
+template <class Eng, int KW, int OUT>
 hipError_t run_one_tile(const Mx4Problem &p, hipStream_t s) {
-  const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN;
-  const int64_t tm = GROUPED ? p.M / Eng::BM + std::min(p.E, p.M) : (p.M + Eng::BM - 1) / Eng::BM;
+  const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN, tm = (p.M + Eng::BM - 1) / Eng::BM;
   const int64_t items = tm * tn * p.slices;
   if (items > INT32_MAX / 2) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(items)), block(Eng::NTHR * KW);
-  if constexpr (GROUPED) {
-    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, false>, Mx4GroupWork<Eng>>), grid, block, 0, s, p);
-  } else if (p.slices > 1) {
-    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, true>, Mx4DenseWork<Eng>>), grid, block, 0, s, p);
+  if (p.slices > 1) {
+    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, true>>), grid, block, 0, s, p);
     return reduce_mx4<OUT>(p, s);
-  } else {
-    hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, false>, Mx4DenseWork<Eng>>), grid, block, 0, s, p);
   }
+  hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, false>>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -560,7 +552,8 @@ hipError_t run_a16(const Mx4Problem &p, int tile, hipStream_t s) {
     case kMx4T256N: return run_tiles<typename Mx4Tiling<kMx4T256N, ACT>::Eng, ACT, GROUPED>(p, s);
     case kMx4T128: return run_tiles<typename Mx4Tiling<kMx4T128, ACT>::Eng, ACT, GROUPED>(p, s);
     case kMx4T64: return run_tiles<typename Mx4Tiling<kMx4T64, ACT>::Eng, ACT, GROUPED>(p, s);
-    case kMx4T32: return run_one_tile<typename Mx4Tiling<kMx4T32, ACT>::Eng, kT32Groups, ACT, GROUPED>(p, s);
+    case kMx4T32:
+      if constexpr (!GROUPED) return run_one_tile<typename Mx4Tiling<kMx4T32, ACT>::Eng, kT32Groups, ACT>(p, s);
     default: return run_stream<ACT, ACT, GROUPED>(p, s);
   }
 }
@@ -572,7 +565,7 @@ hipError_t run_a4(const Mx4Problem &p, int tile, hipStream_t s) {
     case kMx4T256N: return run_tiles<Mx4Tiling<kMx4T256N, kMX4>::Eng, OUT, false>(p, s);
     case kMx4T128: return run_tiles<Mx4Tiling<kMx4T128, kMX4>::Eng, OUT, false>(p, s);
     case kMx4T64: return run_tiles<Mx4Tiling<kMx4T64, kMX4>::Eng, OUT, false>(p, s);
-    case kMx4T32: return run_one_tile<Mx4Tiling<kMx4T32, kMX4>::Eng, kT32Groups, OUT, false>(p, s);
+    case kMx4T32: return run_one_tile<Mx4Tiling<kMx4T32, kMX4>::Eng, kT32Groups, OUT>(p, s);
     default: return run_stream<kMX4, OUT, false>(p, s);
   }
 }
