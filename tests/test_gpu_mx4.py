@@ -354,6 +354,19 @@ def test_grouped_every_kernel_exact_sums(sizes, kernel):
         same(out, ref.rne(c, dtype))
 
 
+@pytest.mark.parametrize("rows,kernel", [(150, "auto"), (1500, "auto"), (6000, "auto"), (6000, "T256")])
+def test_grouped_many_experts(rows, kernel):
+    """300 experts, most of them without rows, some with many."""
+    qg.set_override(mx4_tile=kernel)
+    rng = np.random.default_rng(rows)
+    share = rng.exponential(size=300) ** 6
+    sizes = rng.multinomial(rows, share / share.sum())
+    a, off, B, S, bias, c = grouped_case(rng, sizes, 144, 128, 1, 1)
+    out = torch.full((a.shape[0], 144), 9.0, dtype=BF, device="cuda")
+    qg.gemm_mx4a16_grouped(torch.from_numpy(a).to(BF).cuda(), off, B, S, dev(bias).to(BF), out=out)
+    same(out, ref.rne(c, BF))
+
+
 @pytest.mark.parametrize("kernel", KERNELS)
 def test_grouped_bad_offsets_stay_inside(kernel):
     qg.set_override(mx4_tile=kernel)
@@ -433,6 +446,105 @@ def test_captured_and_replayed(m):
         torch.cuda.synchronize()
         for a, b in zip(outs, step()):
             assert torch.equal(a, b)
+
+
+def test_two_graphs_with_k_slices():
+    """Two captured graphs of a product with K slices, replayed in turn and on
+    two streams at once: neither's partials touch the other's."""
+    rng = np.random.default_rng(21)
+    m, n, k = 128, 256, 4096
+    qg.set_override(mx4_tile="T64", mx4_split=3)
+    assert qg.mx4_workspace_size(m, n, k, 16) > 0
+    B = [tiled(*random_weight(rng, n, k)) for _ in range(2)]
+    x = [torch.randn(m, k, device="cuda", dtype=BF) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i in range(2):
+            qg.gemm_mx4a16(x[i], *B[i])
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            outs.append(qg.gemm_mx4a16(x[i], *B[i]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for r in range(4):
+        for i in range(2):
+            x[i].copy_(torch.randn(m, k, device="cuda", dtype=BF))
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i] if r % 2 else torch.cuda.current_stream()):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], qg.gemm_mx4a16(x[i], *B[i]))
+
+
+# -- operands of 2 GiB and more --------------------------------------------------------
+
+def some_rows(rows, *more):
+    return sorted({0, 1, 255, 256, rows // 2, rows - 257, rows - 256, rows - 17, rows - 1, *more})
+
+
+def device_weight(n, k, seed):
+    """Random tiled codes and scales (bytes 124 .. 126) made on the device."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    c = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = torch.randint(124, 127, (n // 16, (k + 511) // 512, 64, 4), dtype=torch.uint8, device="cuda", generator=g)
+    return c, s
+
+
+def device_rows(c, s, rows):
+    """Their values in the given rows, fp64."""
+    out = []
+    for r in rows:
+        t = r // 16
+        v = qg.dequant_mx4(c[16 * t:16 * t + 16], s[t:t + 1], tiled=True)
+        out.append(host(v)[r % 16])
+    return np.stack(out)
+
+
+def test_a16_activations_past_2gib():
+    m, n, k = 65536 + 300, 80, 16384 + 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    A = torch.empty(m, k, dtype=BF, device="cuda").random_(-4, 5, generator=g)
+    assert A.numel() * 2 > 2 ** 31
+    B = device_weight(n, k, 6)
+    C = qg.gemm_mx4a16(A, *B)
+    r = some_rows(m)
+    # |sum| <= k * 4 * 3 < 2^18 in steps of 2^-4: exact in fp32
+    same(C[r], ref.rne(host(A[r]) @ device_rows(*B, range(n)).T, BF))
+
+
+def test_a4_activations_past_2gib():
+    m, n, k = 131072 + 300, 48, 32768 + 128
+    A, B = device_weight(m + 4, k, 7), device_weight(n, k, 8)
+    assert A[0].numel() > 2 ** 31
+    C = qg.gemm_mx4a4(*A, *B, m=m, out_dtype=SF)
+    most = (2 ** 31 - 1) // (k // 2) // 256 * 256   # rows of one launch
+    r = some_rows(m, most - 1, most, most + 1)
+    a, w = device_rows(*A, r), device_rows(*B, range(n))
+    c = a @ w.T
+    # products in steps of 2^-8, |sum| < 2^19: fp32 rounds each addition
+    assert (np.abs(host(C[r]) - c) <= ref.product_bound(a, w, c, SF)).all()
+
+
+@pytest.mark.parametrize("m", [1, 20])
+def test_weights_past_2gib(m):
+    n, k = 131072 + 48, 32768 + 128
+    B = device_weight(n, k, 9)
+    assert B[0].numel() > 2 ** 31
+    r = some_rows(n)
+    w = device_rows(*B, r)
+    rng = np.random.default_rng(m)
+    a = rng.integers(-4, 5, (m, k)).astype(np.float64)
+    C = qg.gemm_mx4a16(torch.from_numpy(a).to(BF).cuda(), *B)
+    same(C[:, r], ref.rne(a @ w.T, BF))   # |sum| < 2^19 in steps of 2^-4
+    q = qg.quantize_mx4(torch.from_numpy(a).to(BF).cuda(), tiled=True)   # -4 .. 4 are codes' values
+    C = qg.gemm_mx4a4(*q, *B, m=m)
+    same(C[:, r], ref.rne(a @ w.T, BF))
 
 
 def test_two_streams_at_once():

@@ -146,6 +146,30 @@ def test_wrapper_refusals(call):
         call()
 
 
+@pytest.mark.parametrize("call", [
+    lambda e: qg.quantize_mx4(e(1, 2 ** 32 + 128, dtype=torch.bfloat16), tiled=True),
+    lambda e: qg.quantize_mx4(e(2 ** 32 + 1, 32, dtype=torch.float16)),
+    lambda e: qg.dequant_mx4(e(1, 2 ** 31 + 64, dtype=torch.uint8), e(1, 2 ** 27 + 4, dtype=torch.uint8)),
+    lambda e: qg.repack_mx4(e(2 ** 32 + 16, 64, dtype=torch.uint8), e(2 ** 32 + 16, 4, dtype=torch.uint8)),
+    lambda e: qg.gemm_mx4a16(e(2 ** 32 + 1, 128, dtype=torch.float16), e(16, 64, dtype=torch.uint8),
+                             e(1, 1, 64, 4, dtype=torch.uint8)),
+    lambda e: qg.gemm_mx4a16_grouped(e(4, 128, dtype=torch.float16), e(65538, dtype=torch.int32),
+                                     e(65537, 16, 64, dtype=torch.uint8),
+                                     e(65537, 1, 1, 64, 4, dtype=torch.uint8)),
+])
+def test_sizes_past_the_librarys(call):
+    # sizes that a 32-bit integer would wrap (no memory behind them)
+    with pytest.raises(qg.QGemmError) as e:
+        call(lambda *shape, dtype: torch.empty(shape, dtype=dtype, device="meta"))
+    assert e.value.status == 7
+
+
+def test_workspace_size_of_unusable_sizes():
+    for m, n, k, bits in [(2 ** 31 - 1, 256, 4096, 16), (64, 256, 2 ** 31 - 128, 4), (0, 256, 4096, 16),
+                          (64, 250, 4096, 16), (64, 256, 4096, 8), (2 ** 31 - 1, 256, 4096, 4)]:
+        assert qg.mx4_workspace_size(m, n, k, bits) == 0
+
+
 def test_reference_quantizer_examples():
     # one block: largest 7 -> scale 2^0; ties go to the even code
     x = np.zeros((1, 32))

@@ -472,6 +472,14 @@ def _mx4_tiled_shapes(rows: int, k: int) -> tuple:
     return (rt * 16, k // 2), (rt, (k + 511) // 512, 64, 4)
 
 
+_MX4_MOST = 2 ** 31 - 1   # rows, k: the library's sizes are 32-bit
+
+
+def _mx4_size(func: str, rows: int, k: int) -> None:
+    if rows > _MX4_MOST or k > _MX4_MOST:
+        raise QGemmError(func, 7, f"rows and k must be below 2^31 (got {rows} and {k})")
+
+
 def _mx4_multiple(func: str, k: int, step: int) -> None:
     if k % step:
         raise QGemmError(func, 7, f"k must be a multiple of {step} (got {k})")
@@ -527,6 +535,8 @@ def _check_mx4_pair(func: str, codes: torch.Tensor, scales: torch.Tensor, tiled:
     cs = codes.shape
     if codes.dtype == _U8 and scales.dtype == _U8 and len(cs) == len(lead) + 2 and cs[:-2] == lead:
         rows, k = cs[-2], 2 * cs[-1]
+        if rows > _MX4_MOST or k > _MX4_MOST:
+            _mx4_size(func, rows, k)
         if tiled:
             want = lead + ((rows + 15) // 16, (k + 511) // 512, 64, 4)
             if rows % 16 == 0 and k % 128 == 0 and scales.shape == want:
@@ -554,8 +564,9 @@ def quantize_mx4(X: torch.Tensor, tiled: bool = False):
         raise QGemmError(f, _DTYPE, f"X must be bf16, fp16 or fp32 (got {X.dtype})")
     k = X.shape[-1]
     _mx4_multiple(f, k, 128 if tiled else 32)
-    dev = _mx4_devices(f, ((X, "X"),))
     rows = X.numel() // k if k else 0
+    _mx4_size(f, rows, k)
+    dev = _mx4_devices(f, ((X, "X"),))
     shapes = _mx4_tiled_shapes(rows, k) if tiled else ((rows, k // 2), (rows, k // 32))
     codes = X.new_empty(shapes[0], dtype=_U8)
     scales = X.new_empty(shapes[1], dtype=_U8)
@@ -639,6 +650,7 @@ def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
         raise QGemmError(f, _SHAPE, f"A must be [..., {k}] (got {list(A.shape)})")
     _check_bias(f, bias, n)
     m = A.numel() // k if k else 0
+    _mx4_size(f, m, k)
     if out is not None:
         _check_out(f, out, A.dtype, m, n)
     dev = _mx4_devices(f, ((A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
@@ -705,6 +717,8 @@ def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.T
     rows = A.shape[0]
     if A.shape[1] != k:
         raise QGemmError(f, _SHAPE, f"A must be [rows, {k}] (got {list(A.shape)})")
+    _mx4_size(f, rows, k)
+    _need(E <= 65536, f, 7, f"at most 65536 experts (got {E})")
     if bias is not None:
         _need(bias.dtype in _ACT, f, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
         _need(_shape(bias) == (E, n), f, _SHAPE, f"bias must be [{E}, {n}] (got {list(bias.shape)})")

@@ -379,7 +379,8 @@ qg_status qunrepack_mx4(const uint8_t *codes_t, const uint8_t *scales_t, uint8_t
 }
 
 size_t qgemm_mx4_workspace_size(int m, int n, int k, int act_bits) {
-  if (m <= 0 || n <= 0 || k <= 0 || n % 16 != 0 || k % 128 != 0 || (act_bits != 16 && act_bits != 4))
+  if (m <= 0 || n <= 0 || k <= 0 || n % 16 != 0 || k % 128 != 0 || m > INT32_MAX - 255 ||
+      n > INT32_MAX - 255 || k > INT32_MAX - 511 || (act_bits != 16 && act_bits != 4))
     return 0;
   const size_t b = qg::mx4_workspace_bytes(m, n, k, act_bits);
   return b ? (b + 255) & ~static_cast<size_t>(255) : 0;

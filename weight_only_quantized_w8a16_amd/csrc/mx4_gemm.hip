@@ -357,6 +357,7 @@ hipError_t run_stream_as(const Mx4Problem &p, long slabs, hipStream_t s) {
   const int nb = p.K >> 7, waves = nb < 8 ? nb : 8;
   const size_t lds = static_cast<size_t>(waves) * NT * 256 * sizeof(float);
   const unsigned cols = static_cast<unsigned>(((p.N >> 4) + NT - 1) / NT);
+  if (static_cast<uint64_t>(cols) * 64 * waves > UINT32_MAX) return hipErrorInvalidValue;
   for (long s0 = 0; s0 < slabs; s0 += kMaxSlabs) {
     const unsigned ny = static_cast<unsigned>(std::min<long>(slabs - s0, kMaxSlabs));
     hipLaunchKernelGGL((k_mx4_stream<ACT, OUT, NT, GROUPED, DEPTH>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
@@ -427,6 +428,14 @@ constexpr Mx4Cost kCost4[] = {{256, 256, 1, 10.2f, 0.336f, 0.077f, 0.504f},
 // K slices: the reduction's launch, and a byte of partials (in the same fit).
 constexpr float kSliceLaunch = 2.3f, kSliceByte = 2.8e-7f;
 
+// 32-bit offsets of the tile kernels stay below this, and with MX4 activations
+// a launch takes at most so many rows (K from 2^22 on streams: no limit).
+constexpr uint64_t kMx4Span = uint64_t(1) << 31;
+int mx4_rows_most(int K, bool a4) {
+  if (!a4 || K >= 1 << 22) return INT32_MAX;
+  return static_cast<int>(std::min<uint64_t>((kMx4Span - 1) / (static_cast<uint64_t>(K) / 2), INT32_MAX)) / 256 * 256;
+}
+
 struct Mx4Plan {
   int tile;            // Mx4Kernel
   int kseg, slices;    // K slices in 512-k windows
@@ -454,11 +463,14 @@ float tiles_time(const Mx4Cost &c, float tiles, float steps) {
 Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   Mx4Plan pl{kMx4Stream, 0, 1, 0};
   const Override ov = dispatch_override();
-  // 32-bit offsets of the tile kernels' buffer loads and stores: the operands,
-  // and a tile's rows of C (or of fp32 partials).
-  const uint64_t lim = uint64_t(1) << 31;
-  const uint64_t a_bytes = uint64_t((M + 15) / 16 * 16) * K / (a4 ? 2 : 1) * (a4 ? 1 : 2);
-  if (a_bytes >= lim || uint64_t(N) * K / 2 >= lim || uint64_t(N) * 4 * 256 >= lim) return pl;
+  // The tile kernels' buffer loads and stores have 32-bit offsets.  They span a
+  // tile's rows of C (or of fp32 partials), an expert's scales, and with
+  // 16-bit activations the tile's rows of A and its channels' codes; with MX4
+  // ones all codes of B (and of A: launch_mx4_gemm takes its rows in parts).
+  const uint64_t lim = kMx4Span, windows64 = mx4_scale_windows(K) * uint64_t(256);
+  if (uint64_t(256) * 4 * N >= lim || (N / 16) * windows64 >= lim || uint64_t(256) * K * 2 >= lim ||
+      (a4 && uint64_t(N) * K / 2 >= lim))
+    return pl;
   const Mx4Cost *cost = a4 ? kCost4 : kCost16;
   const int windows = mx4_scale_windows(K);
   if (ov.mx4_tile >= 0 && !(grouped && ov.mx4_tile == kMx4T32)) {
@@ -535,7 +547,7 @@ template <class Eng, int KW, int OUT>
 hipError_t run_one_tile(const Mx4Problem &p, hipStream_t s) {
   const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN, tm = (p.M + Eng::BM - 1) / Eng::BM;
   const int64_t items = tm * tn * p.slices;
-  if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+  if (items * Eng::NTHR * KW > UINT32_MAX) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(items)), block(Eng::NTHR * KW);
   if (p.slices > 1) {
     hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, true>>), grid, block, 0, s, p);
@@ -570,31 +582,47 @@ hipError_t run_a4(const Mx4Problem &p, int tile, hipStream_t s) {
   }
 }
 
+hipError_t run_mx4(const Mx4Problem &p, const Mx4Args &a, int tile, hipStream_t s) {
+  if (a.act == kMX4) {
+    switch (a.out) {
+      case QG_FP32: return run_a4<QG_FP32>(p, tile, s);
+      case QG_FP16: return run_a4<QG_FP16>(p, tile, s);
+      default: return run_a4<QG_BF16>(p, tile, s);
+    }
+  }
+  if (a.offsets) return a.act == kFP16 ? run_a16<kFP16, true>(p, tile, s) : run_a16<kBF16, true>(p, tile, s);
+  return a.act == kFP16 ? run_a16<kFP16, false>(p, tile, s) : run_a16<kBF16, false>(p, tile, s);
+}
+
 }  // namespace
 
 size_t mx4_workspace_bytes(int m, int n, int k, int act_bits) {
-  return plan_mx4(m, n, k, act_bits == 4, false, 0).bytes;
+  const bool a4 = act_bits == 4;
+  return plan_mx4(std::min(m, mx4_rows_most(k, a4)), n, k, a4, false, 0).bytes;
 }
 
 hipError_t launch_mx4_gemm(const Mx4Args &a, hipStream_t s) {
-  Mx4Problem p{a.A, reinterpret_cast<const uint32_t *>(a.AS), a.B, reinterpret_cast<const uint32_t *>(a.BS),
-               a.bias, a.C, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, nullptr, 0, 1};
-  const Mx4Plan pl = plan_mx4(a.M, a.N, a.K, a.act == kMX4, a.offsets != nullptr, a.E);
-  if (pl.slices > 1 && a.ws && a.ws_bytes >= pl.bytes) {
-    p.part = static_cast<float *>(a.ws);
-    p.kseg = pl.kseg;
-    p.slices = pl.slices;
-  }
-  if (a.act == kMX4) {
-    switch (a.out) {
-      case QG_FP32: return run_a4<QG_FP32>(p, pl.tile, s);
-      case QG_FP16: return run_a4<QG_FP16>(p, pl.tile, s);
-      default: return run_a4<QG_BF16>(p, pl.tile, s);
+  const bool a4 = a.act == kMX4;
+  const int most = mx4_rows_most(a.K, a4);
+  for (int64_t m0 = 0; m0 < a.M; m0 += most) {
+    const int M = static_cast<int>(std::min<int64_t>(a.M - m0, most));
+    const Mx4Plan pl = plan_mx4(M, a.N, a.K, a4, a.offsets != nullptr, a.E);
+    Mx4Problem p{a.A, reinterpret_cast<const uint32_t *>(a.AS), a.B, reinterpret_cast<const uint32_t *>(a.BS),
+                 a.bias, a.C, M, a.N, a.K, a.bias_dt, a.offsets, a.E, nullptr, 0, 1};
+    if (m0) {   // MX4 activations, a multiple of 256 rows in
+      p.A = static_cast<const uint8_t *>(a.A) + static_cast<size_t>(m0) * a.K / 2;
+      p.AS += static_cast<size_t>(m0 / 16) * mx4_scale_windows(a.K) * 64;
+      p.C = static_cast<char *>(a.C) + static_cast<size_t>(m0) * a.N * (a.out == QG_FP32 ? 4 : 2);
     }
+    if (pl.slices > 1 && a.ws && a.ws_bytes >= pl.bytes) {
+      p.part = static_cast<float *>(a.ws);
+      p.kseg = pl.kseg;
+      p.slices = pl.slices;
+    }
+    const hipError_t e = run_mx4(p, a, pl.tile, s);
+    if (e != hipSuccess) return e;
   }
-  if (a.offsets)
-    return a.act == kFP16 ? run_a16<kFP16, true>(p, pl.tile, s) : run_a16<kBF16, true>(p, pl.tile, s);
-  return a.act == kFP16 ? run_a16<kFP16, false>(p, pl.tile, s) : run_a16<kBF16, false>(p, pl.tile, s);
+  return hipSuccess;
 }
 
 }  // namespace qg

@@ -113,9 +113,9 @@ struct Mx4RowBuffer {
 // long as both operands use the same): of the codes, word ks of the lane's 16
 // bytes; of the activations, chunk 4 h + ks of the row.
 //
-// Rows past the end of A and channel tiles past the end of B fall outside the
-// buffer resources and read as zeros (a grouped product also reads on into
-// the next expert's rows); their outputs are not stored.
+// The buffer resources of the loads span the tile's rows and channels: rows
+// and channel tiles past the last one read as zeros, their outputs are not
+// stored, and offsets stay small however large the matrices are.
 // ---------------------------------------------------------------------------
 template <int ACT_, int BM_, int BN_, int WM_, int WN_, int NS_, bool PRE>
 struct Mx4Engine16 {
@@ -163,14 +163,15 @@ struct Mx4Engine16 {
 
   __device__ __forceinline__ void issue(char *stage, const Mx4Item &t, int step) const {
     const auto rA = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<void *>(p.A), 0, static_cast<int>(static_cast<uint32_t>(p.M) * static_cast<uint32_t>(p.K) * 2u),
-        kRsrcFlags);
+        const_cast<char *>(static_cast<const char *>(p.A) + static_cast<size_t>(t.row_lo) * p.K * 2), 0,
+        static_cast<int>(static_cast<uint32_t>(t.row_last - t.row_lo + 1) * static_cast<uint32_t>(p.K) * 2u), kRsrcFlags);
     const auto rB = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t *>(p.B + static_cast<size_t>(t.e) * ntiles * nb * 1024), 0,
-        static_cast<int>(static_cast<uint32_t>(ntiles) * static_cast<uint32_t>(nb) * 1024u), kRsrcFlags);
+        const_cast<uint8_t *>(p.B + (static_cast<size_t>(t.e) * ntiles + (t.col_lo >> 4)) * nb * 1024), 0,
+        static_cast<int>(static_cast<uint32_t>(min(BN / 16, ntiles - (t.col_lo >> 4))) * static_cast<uint32_t>(nb) * 1024u),
+        kRsrcFlags);
 #pragma unroll
     for (int i = 0; i < A_DMA; ++i) {
-      const uint32_t row = static_cast<uint32_t>(t.row_lo + 8 * (wave * A_DMA + i));
+      const uint32_t row = static_cast<uint32_t>(8 * (wave * A_DMA + i));
       const int off = static_cast<int>(a_lane[i & 1] + row * static_cast<uint32_t>(p.K) * 2u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, lds_ptr(stage + (wave * A_DMA + i) * 1024), 16, off, step * 128, 0, 0);
     }
@@ -179,7 +180,7 @@ struct Mx4Engine16 {
       // With fewer code loads than waves, waves repeat one (the same bytes to
       // the same place).
       const int b = (wave * B_DMA + i) % B_LOADS;
-      const uint32_t tile = static_cast<uint32_t>((t.col_lo >> 4) + 2 * b);
+      const uint32_t tile = static_cast<uint32_t>(2 * b);
       const int off = static_cast<int>(b_lane + tile * static_cast<uint32_t>(nb) * 1024u);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, lds_ptr(stage + STAGE_A + b * 1024), 16, off, step * 512, 0, 0);
     }
