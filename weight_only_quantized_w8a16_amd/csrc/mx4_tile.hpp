@@ -677,6 +677,10 @@ __device__ __forceinline__ void mx4_tiles(const Mx4Problem &p, Work &work, const
     eng.clear();
     typename Out::template Bias<Eng::WTN> bias;
     bias.load(p, ci, ci.col_lo + eng.wn * Eng::WTN);
+    // A wave whose rows all lie past the tile's last multiplies nothing (its
+    // loads and barriers are the workgroup's).  Grouped, 2048 rows over 64
+    // experts on 128 x 256 tiles: 78 -> 68 us, 12288 rows 160 -> 155.
+    const int end = ci.row_lo + eng.wm * Eng::WTM <= ci.row_last ? ci.s1 : ci.s0;
     for (int s = ci.s0; s < ci.s1; s += W) {
       // The window after this one: of this tile, or the next tile's first.
       const bool last = s + W >= ci.s1;
@@ -694,7 +698,7 @@ __device__ __forceinline__ void mx4_tiles(const Mx4Problem &p, Work &work, const
       // but its stores and this window's scale loads.
       auto body = [&](auto Ic) {
         constexpr int I = decltype(Ic)::value, ST = I % NS, AHEAD = I + NS;
-        const bool live = s + I < ci.s1;
+        const bool live = s + I < end;
         __builtin_amdgcn_sched_barrier(0);
         if (live) eng.template first<I>(L.s[ST], f[I & 1], cur);
         __builtin_amdgcn_sched_barrier(0);
