@@ -1,6 +1,8 @@
 // mx4_gemm.hip -- products with MX4 weights:
 //   C[m, n] = sum_k A[m, k] * value(B)[n, k] (+ bias[n]),
-// A in 16 bits or MX4, dense or grouped by expert (include/qgemm.h).
+// A in 16 bits or MX4, dense or grouped by expert (include/qgemm.h).  Sums are
+// fp32; the one rounding is the store to C's type (and in fp16 that of a
+// weight below 2^-23 or from 65520 on, as the conversion's).
 //
 // Every block of 32 weights has a power-of-two scale, so a scaled weight is
 // exact in bf16 and the conversion instructions apply the scale while they
@@ -98,7 +100,9 @@ __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4])
 // one 32-value block.  Nothing is shared between waves until their sums meet
 // in LDS, so no wave waits for another's loads.  Bound by HBM; row blocks of
 // 32 and 64 were slower than the tiles (every wave reads its activations out
-// of L2 by itself).
+// of L2 by itself).  Measured: M = 1, N = 131072, K = 2048 (142.6 MB) 23.6 us,
+// 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 12.3 us; MX4 activations of 8
+// rows there 8.5; 48 rows over 64 experts of 2816 x 2048 18.9.
 // ---------------------------------------------------------------------------
 // 4 x 4 transpose over the four 16-lane rows of a wave: a[t] of lane row j and
 // a[j] of lane row t trade places.
@@ -309,6 +313,9 @@ struct Mx4GroupWork {
   }
 };
 
+// bf16 activations, 2048 x 13312 x 2048: 90.5 us (1.23 PFLOP/s) on 256 x 256
+// tiles, 12288 rows over 64 experts of 2816 x 2048 153 us (0.93) on 128 x 256;
+// MX4 activations, 4096 x 18944 x 3584: 144 to 150 us (3.7 to 3.9).
 template <class Eng, class Out, class Work>
 __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem p) {
   __shared__ __attribute__((aligned(16))) char s0[Eng::STAGE];
@@ -321,6 +328,7 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem 
   mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3}, ep, bias});
 }
 
+// 100 x 3584 x 3584: 9.1 us, against 17.0 on 64 x 128 tiles in two K slices.
 template <class Eng, int KW, class Out>
 __global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
   __shared__ __attribute__((aligned(16))) float bias[Eng::NW * Eng::WTN];
@@ -334,6 +342,8 @@ __global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
 }
 
 // K slices: C = RNE_out(the slices' partials summed in slice order + bias).
+// Bound by the partials' traffic out of MALL: three slices of 333 x 3584
+// (14.3 MB) 4.9 us.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_mx4_reduce(Mx4Problem p) {
   const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
@@ -456,10 +466,14 @@ float tiles_time(const Mx4Cost &c, float tiles, float steps) {
 // row padding beyond 16 (m = 13, n = 18944, k = 3584: 13.6 us against 15.0 on
 // 32 x 64 tiles; m = 32: 20.4 against 16.8).  A grouped product's row tiles
 // are not known to the host: it reckons with half a tile too many for every
-// expert, takes no 32-row tiles (2048 rows over 64 experts, n = 2816, k = 2048:
-// 85.6 us against 64.6 on 64-row ones), and streams up to a mean of 12 rows an
-// expert (512 rows: 45.7 us against 49.9 on 64-row tiles, 1024 rows 62.9
-// against 58.8).
+// expert (on 27 sizes of 12 to 256 rows an expert, 8 to 128 experts, the tile
+// so picked is within 1 % of the best on average, 16 % at worst) and takes no
+// 32-row tiles (2048 rows over 64 experts, n = 2816, k = 2048: 85.6 us against
+// 64.6 on 64-row ones).  It streams up to a mean of 7 rows an expert (64
+// experts, n = 2048, k = 1408: 6 rows each 23.7 us against 26.3 on 64-row
+// tiles, 8 rows 26.8 against 25.9, 12 rows 31.9 against 27.6), or of 12 up to
+// 96 rows in all (8 experts, n = 3584, k = 2560: 8 rows each 12.6 against
+// 16.5, 12 rows 17.4 against 17.9).
 Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   Mx4Plan pl{kMx4Stream, 0, 1, 0};
   const Override ov = dispatch_override();
@@ -475,7 +489,7 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   const int windows = mx4_scale_windows(K);
   if (ov.mx4_tile >= 0 && !(grouped && ov.mx4_tile == kMx4T32)) {
     pl.tile = ov.mx4_tile;
-  } else if (grouped ? M > 12 * static_cast<int64_t>(E) : M > 16) {
+  } else if (M > (grouped ? std::max<int64_t>(7 * int64_t(E), std::min<int64_t>(12 * int64_t(E), 96)) : 16)) {
     float best = 0.f;
     for (int i = 0; i < (grouped ? 4 : 5); ++i) {
       const int64_t cols = (N + cost[i].bn - 1) / cost[i].bn;
