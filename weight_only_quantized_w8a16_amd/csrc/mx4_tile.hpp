@@ -117,7 +117,7 @@ struct Mx4RowBuffer {
 // and channel tiles past the last one read as zeros, their outputs are not
 // stored, and offsets stay small however large the matrices are.
 //
-// Bound by the matrix cores: the 256 x 256 tile runs at 1.4 PFLOP/s while it
+// Bound by the matrix cores: the 256 x 256 tile runs at 1.4 to 1.6 PFLOP/s while it
 // multiplies, an endless loop of these instructions with nothing else at 1.85
 // (the chip lowers its clock under either).
 // ---------------------------------------------------------------------------
