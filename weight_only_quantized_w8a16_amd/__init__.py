@@ -95,14 +95,16 @@ def _check_groups(func: str, name: str, t: torch.Tensor, dtype, rows: int, k: in
 
 
 def _check_out(func: str, out: torch.Tensor, dtype, m: int, n: int) -> None:
+    if out.dtype == dtype and out.dim() >= 1 and out.shape[-1] == n and out.numel() == m * n:
+        return   # without building the messages below
     _need(out.dtype == dtype, func, _DTYPE, f"out must be {dtype} (got {out.dtype})")
     _need(out.dim() >= 1 and out.shape[-1] == n and out.numel() == m * n, func, _SHAPE,
           f"out must hold [{m}, {n}] (got {list(out.shape)})")
 
 
 def _check_bias(func: str, bias: Optional[torch.Tensor], n: int) -> None:
-    if bias is None:
-        return
+    if bias is None or (bias.dtype in _ACT and bias.shape == (n,)):
+        return   # without building the messages below
     _need(bias.dtype in _ACT, func, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
     _need(_shape(bias) == (n,), func, _SHAPE, f"bias must be [{n}] (got {list(bias.shape)})")
 
@@ -485,18 +487,18 @@ def _mx4_multiple(func: str, k: int, step: int) -> None:
         raise QGemmError(func, 7, f"k must be a multiple of {step} (got {k})")
 
 
-def _mx4_devices(func: str, named) -> int:
-    """The device index the given (tensor, name) pairs share; None is skipped.
-    Raises for tensors off the device, on another one, or not contiguous."""
-    dev = named[0][0].get_device()
-    for t, _ in named:
+def _mx4_devices(func: str, tensors: tuple, names: tuple) -> int:
+    """The device index the given tensors share; None is skipped.  Raises for
+    tensors off the device, on another one, or not contiguous."""
+    dev = tensors[0].get_device()
+    for t in tensors:
         if t is not None and not (t.get_device() == dev and t.is_contiguous()):
             break
     else:
         if dev >= 0:
             return dev
     dev = None
-    for t, name in named:
+    for t, name in zip(tensors, names):
         if t is None:
             continue
         if not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
@@ -532,19 +534,19 @@ def _mx4_call(func: str, dev: int, *args) -> None:
 def _check_mx4_pair(func: str, codes: torch.Tensor, scales: torch.Tensor, tiled: bool,
                     names=("codes", "scales"), lead: tuple = ()) -> tuple:
     """(rows held, k) of a codes / scales pair (after the leading dimensions)."""
-    cs = codes.shape
-    if codes.dtype == _U8 and scales.dtype == _U8 and len(cs) == len(lead) + 2 and cs[:-2] == lead:
-        rows, k = cs[-2], 2 * cs[-1]
+    cs, at = codes.shape, len(lead)
+    if codes.dtype == _U8 and scales.dtype == _U8 and len(cs) == at + 2 and (at == 0 or cs[:at] == lead):
+        rows, k = cs[at], 2 * cs[at + 1]
         if rows > _MX4_MOST or k > _MX4_MOST:
             _mx4_size(func, rows, k)
         if tiled:
-            want = lead + ((rows + 15) // 16, (k + 511) // 512, 64, 4)
+            want = (*lead, (rows + 15) // 16, (k + 511) // 512, 64, 4)
             if rows % 16 == 0 and k % 128 == 0 and scales.shape == want:
                 return rows, k
             _need(rows % 16 == 0, func, 7, f"{names[0]} must hold whole 16-row tiles (got {rows} rows)")
             _mx4_multiple(func, k, 128)
         else:
-            want = lead + (rows, k // 32)
+            want = (*lead, rows, k // 32)
             if k % 32 == 0 and scales.shape == want:
                 return rows, k
             _mx4_multiple(func, k, 32)
@@ -566,7 +568,7 @@ def quantize_mx4(X: torch.Tensor, tiled: bool = False):
     _mx4_multiple(f, k, 128 if tiled else 32)
     rows = X.numel() // k if k else 0
     _mx4_size(f, rows, k)
-    dev = _mx4_devices(f, ((X, "X"),))
+    dev = _mx4_devices(f, (X,), ("X",))
     shapes = _mx4_tiled_shapes(rows, k) if tiled else ((rows, k // 2), (rows, k // 32))
     codes = X.new_empty(shapes[0], dtype=_U8)
     scales = X.new_empty(shapes[1], dtype=_U8)
@@ -586,7 +588,7 @@ def dequant_mx4(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtyp
     rows = held if rows is None else rows
     if not 0 <= rows <= held:
         raise QGemmError(f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
-    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
+    dev = _mx4_devices(f, (codes, scales), ("codes", "scales"))
     out = codes.new_empty((rows, k), dtype=out_dtype)
     _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), rows, k,
               QG_LAYOUT_TILED if tiled else QG_LAYOUT_PORTABLE, _CODES[out_dtype], _mx4_stream(dev))
@@ -598,7 +600,7 @@ def repack_mx4(codes: torch.Tensor, scales: torch.Tensor):
     f = "qrepack_mx4"
     rows, k = _check_mx4_pair(f, codes, scales, False)
     _mx4_multiple(f, k, 128)
-    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
+    dev = _mx4_devices(f, (codes, scales), ("codes", "scales"))
     shapes = _mx4_tiled_shapes(rows, k)
     tc = torch.empty(shapes[0], dtype=_U8, device=codes.device)
     ts = torch.empty(shapes[1], dtype=_U8, device=codes.device)
@@ -613,7 +615,7 @@ def unrepack_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: Optional[int] 
     rows = held if rows is None else rows
     if not 0 <= rows <= held:
         raise QGemmError(f, _SHAPE, f"rows must be in [0, {held}] (got {rows})")
-    dev = _mx4_devices(f, ((codes, "codes"), (scales, "scales")))
+    dev = _mx4_devices(f, (codes, scales), ("codes", "scales"))
     pc = torch.empty((rows, k // 2), dtype=_U8, device=codes.device)
     ps = torch.empty((rows, k // 32), dtype=_U8, device=codes.device)
     _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), pc.data_ptr(), ps.data_ptr(), rows, k, _mx4_stream(dev))
@@ -646,21 +648,29 @@ def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
     if A.dtype not in _ACT or A.dim() < 1:
         raise QGemmError(f, _DTYPE, f"A must be bf16 or fp16 (got {A.dtype})")
     n, k = _check_mx4_pair(f, B_tiled, B_scales, True, ("B_tiled", "B_scales"))
-    if A.shape[-1] != k:
+    lead = A.shape
+    if lead[-1] != k:
         raise QGemmError(f, _SHAPE, f"A must be [..., {k}] (got {list(A.shape)})")
-    _check_bias(f, bias, n)
-    m = A.numel() // k if k else 0
-    _mx4_size(f, m, k)
+    if bias is not None:
+        _check_bias(f, bias, n)
+    if len(lead) == 2 and k:
+        m = lead[0]
+        lead = (m,)
+    else:
+        m = A.numel() // k if k else 0
+        lead = lead[:-1]
+    if m > _MX4_MOST:
+        _mx4_size(f, m, k)
     if out is not None:
         _check_out(f, out, A.dtype, m, n)
-    dev = _mx4_devices(f, ((A, "A"), (B_tiled, "B_tiled"), (B_scales, "B_scales"), (bias, "bias"),
-                           (out, "out"), (workspace, "workspace")))
-    C = out if out is not None else A.new_empty((*A.shape[:-1], n))
+    dev = _mx4_devices(f, (A, B_tiled, B_scales, bias, out, workspace),
+                       ("A", "B_tiled", "B_scales", "bias", "out", "workspace"))
+    C = out if out is not None else A.new_empty((*lead, n))
     ws, ws_ptr, ws_bytes = _mx4_workspace(m, n, k, 16, A, workspace)
     _mx4_call(f, dev, A.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias), C.data_ptr(), m, n, k,
               _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype], ws_ptr, ws_bytes,
               _mx4_stream(dev))
-    return C if out is None else C.reshape(*A.shape[:-1], n)
+    return C if out is None else C.reshape(*lead, n)
 
 
 def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Tensor,
@@ -684,9 +694,8 @@ def gemm_mx4a4(A_tiled: torch.Tensor, A_scales: torch.Tensor, B_tiled: torch.Ten
         _check_out(f, out, out_dtype, m, n)
     if out_dtype not in _CODES:
         raise QGemmError(f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
-    dev = _mx4_devices(f, ((A_tiled, "A_tiled"), (A_scales, "A_scales"), (B_tiled, "B_tiled"),
-                           (B_scales, "B_scales"), (bias, "bias"), (out, "out"),
-                           (workspace, "workspace")))
+    dev = _mx4_devices(f, (A_tiled, A_scales, B_tiled, B_scales, bias, out, workspace),
+                       ("A_tiled", "A_scales", "B_tiled", "B_scales", "bias", "out", "workspace"))
     C = out if out is not None else A_tiled.new_empty((m, n), dtype=out_dtype)
     ws, ws_ptr, ws_bytes = _mx4_workspace(m, n, k, 4, A_tiled, workspace)
     _mx4_call(f, dev, A_tiled.data_ptr(), A_scales.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias),
@@ -718,14 +727,15 @@ def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.T
     if A.shape[1] != k:
         raise QGemmError(f, _SHAPE, f"A must be [rows, {k}] (got {list(A.shape)})")
     _mx4_size(f, rows, k)
-    _need(E <= 65536, f, 7, f"at most 65536 experts (got {E})")
-    if bias is not None:
+    if E > 65536:
+        raise QGemmError(f, 7, f"at most 65536 experts (got {E})")
+    if bias is not None and not (bias.dtype in _ACT and bias.shape == (E, n)):
         _need(bias.dtype in _ACT, f, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
         _need(_shape(bias) == (E, n), f, _SHAPE, f"bias must be [{E}, {n}] (got {list(bias.shape)})")
     if out is not None:
         _check_out(f, out, A.dtype, rows, n)
-    dev = _mx4_devices(f, ((A, "A"), (offsets, "offsets"), (B_tiled, "B_tiled"),
-                           (B_scales, "B_scales"), (bias, "bias"), (out, "out")))
+    dev = _mx4_devices(f, (A, offsets, B_tiled, B_scales, bias, out),
+                       ("A", "offsets", "B_tiled", "B_scales", "bias", "out"))
     C = out if out is not None else A.new_empty((rows, n))
     _mx4_call(f, dev, A.data_ptr(), offsets.data_ptr(), B_tiled.data_ptr(), B_scales.data_ptr(), _ptr(bias), C.data_ptr(),
               rows, n, k, E, _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype],
