@@ -101,7 +101,7 @@ __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4])
 // in LDS, so no wave waits for another's loads.  Bound by HBM; row blocks of
 // 32 and 64 were slower than the tiles (every wave reads its activations out
 // of L2 by itself).  Measured: M = 1, N = 131072, K = 2048 (142.6 MB) 23.6 us,
-// 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 12.3 us; MX4 activations of 8
+// 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 9.8 us; MX4 activations of 8
 // rows there 8.5; 48 rows over 64 experts of 2816 x 2048 18.9.
 // ---------------------------------------------------------------------------
 // 4 x 4 transpose over the four 16-lane rows of a wave: a[t] of lane row j and
@@ -375,24 +375,42 @@ hipError_t run_stream_as(const Mx4Problem &p, long slabs, hipStream_t s) {
   }
   return hipGetLastError();
 }
-// Column tiles a workgroup: one while there are few (each workgroup a CU's
-// share; two blocks' loads in flight a wave), two or four when there are many,
-// so that a workgroup's activations, its start and its final sum serve more
-// weight bytes.  Measured at M = 1: N = 2048 3.6 us with one, 4.1 with two;
-// N = 18944 (K = 3584) 12.5 with one, 10.8 with two or four; N = 131072 38,
-// 26.7 and 24.2 (5.9 TB/s of weights); M = 13, N = 18944 17.8, 13.2 and 12.9.
-// MX4 activations weigh less: M = 8, N = 18944 9.2 with two, 10.4 with four.
-// Depth two with one tile: N = 3584, K = 3584 5.0 -> 4.6 us, MX4 activations
-// at K = 18944 14.3 -> 11.7; with more tiles it gains nothing.
+// Column tiles a workgroup (NT): as many as let every CU have one workgroup,
+// up to six, then half as many (two rounds of workgroups) up to five, then
+// four: a round that a few workgroups overhang costs nearly as much as a full
+// one.  Measured with NT from 1 on, K = 3584 unless stated:
+//   tiles / CUs 1.0  (N = 4096, K = 4096, M = 4)   5.1  5.9  6.7  7.2
+//               1.25 (N = 5120, K = 5120, M = 8)  10.2  7.2  8.3  8.8
+//               2.5  (N = 10240, K = 2048, M = 1)  5.8  5.8  5.2  5.3  5.7
+//               3.25 (N = 13312, K = 2048, M = 12) 9.3  7.1  7.9  6.2  6.7  7.2
+//               4.6  (N = 18944, M = 13)          17.7 13.2 12.1 12.9  9.8 10.6
+//               6.0  (N = 24576, K = 2048, M = 16) 14.9 10.9  9.1 9.5 10.6  8.5
+//               7.0  (N = 28672, K = 4096, M = 1) 18.5 14.0 13.8 12.9 14.8 16.5
+//               32   (N = 131072, K = 2048, M = 1) 35 26.4 24.8 23.9 24.4 24.7
+// MX4 activations alike (4.6, M = 8: 9.9 9.3 8.9 10.3 8.5 8.7).  One column
+// tile keeps two blocks' loads in flight (N = 3584 5.0 -> 4.6 us); with more it
+// gains nothing.  A grouped product's workgroups are bounds, most without rows:
+// one, two or four (48 rows over 64 experts of 2816 x 2048 29, 20 and 18 us).
 template <int ACT, int OUT, bool GROUPED>
 hipError_t run_stream(const Mx4Problem &p, hipStream_t s) {
   // Row slabs: a grouped product has at most one partial slab per expert
   // with rows.
   const long slabs = GROUPED ? p.M / 16 + std::min(p.E, p.M) : (p.M + 15) / 16;
-  const long tiles = (p.N >> 4) * slabs;
-  if (tiles < 512) return run_stream_as<ACT, OUT, 1, GROUPED, 2>(p, slabs, s);
-  if (tiles < 1024 || (tiles < 4096 && ACT == kMX4)) return run_stream_as<ACT, OUT, 2, GROUPED, 1>(p, slabs, s);
-  return run_stream_as<ACT, OUT, 4, GROUPED, 1>(p, slabs, s);
+  const long cus = device_cus(), rounds = ((p.N >> 4) * slabs + cus - 1) / cus;
+  if constexpr (GROUPED) {
+    if (rounds <= 2) return run_stream_as<ACT, OUT, 1, true, 2>(p, slabs, s);
+    if (rounds <= 4) return run_stream_as<ACT, OUT, 2, true, 1>(p, slabs, s);
+    return run_stream_as<ACT, OUT, 4, true, 1>(p, slabs, s);
+  } else {
+    switch (rounds <= 6 ? rounds : rounds <= 10 ? (rounds + 1) / 2 : 4) {
+      case 1: return run_stream_as<ACT, OUT, 1, false, 2>(p, slabs, s);
+      case 2: return run_stream_as<ACT, OUT, 2, false, 1>(p, slabs, s);
+      case 3: return run_stream_as<ACT, OUT, 3, false, 1>(p, slabs, s);
+      case 4: return run_stream_as<ACT, OUT, 4, false, 1>(p, slabs, s);
+      case 5: return run_stream_as<ACT, OUT, 5, false, 1>(p, slabs, s);
+      default: return run_stream_as<ACT, OUT, 6, false, 1>(p, slabs, s);
+    }
+  }
 }
 
 }  // namespace
