@@ -439,20 +439,22 @@ constexpr int kT32Groups = 4;
 // to 4096 rows and eight weight shapes of 512 x 2048 to 18944 x 3584, each
 // tile and slice count forced (residual 6 to 8 %); the tile it picks is within
 // 3 % of the best one on average, 29 % at worst.
+// 32 x 64 tiles, one a workgroup, pay a start (again) for every further round
+// (32 x 131072 x 2048: 48 us against 35.6 on 64 x 128 tiles).
 struct Mx4Cost {
   int bm, bn, most;
-  float t0, lone, shared, full;
+  float t0, lone, shared, full, again;
 };
-constexpr Mx4Cost kCost16[] = {{256, 256, 1, 10.9f, 0.988f, 0.303f, 1.534f},
-                               {128, 256, 1, 7.3f, 0.550f, 0.173f, 0.819f},
-                               {128, 128, 2, 4.8f, 0.394f, 0.221f, 0.880f},
-                               {64, 128, 2, 5.5f, 0.228f, 0.120f, 0.505f},
-                               {32, 64, 2, 5.5f, 0.045f, 0.069f, 0.200f}};
-constexpr Mx4Cost kCost4[] = {{256, 256, 1, 10.2f, 0.336f, 0.077f, 0.504f},
-                              {128, 256, 1, 6.8f, 0.218f, 0.077f, 0.302f},
-                              {128, 128, 2, 6.0f, 0.140f, 0.073f, 0.319f},
-                              {64, 128, 2, 5.1f, 0.105f, 0.048f, 0.207f},
-                              {32, 64, 2, 5.6f, 0.029f, 0.037f, 0.123f}};
+constexpr Mx4Cost kCost16[] = {{256, 256, 1, 10.9f, 0.988f, 0.303f, 1.534f, 0.f},
+                               {128, 256, 1, 7.3f, 0.550f, 0.173f, 0.819f, 0.f},
+                               {128, 128, 2, 4.8f, 0.394f, 0.221f, 0.880f, 0.f},
+                               {64, 128, 2, 5.5f, 0.228f, 0.120f, 0.505f, 0.f},
+                               {32, 64, 2, 5.5f, 0.045f, 0.069f, 0.200f, 3.5f}};
+constexpr Mx4Cost kCost4[] = {{256, 256, 1, 10.2f, 0.336f, 0.077f, 0.504f, 0.f},
+                              {128, 256, 1, 6.8f, 0.218f, 0.077f, 0.302f, 0.f},
+                              {128, 128, 2, 6.0f, 0.140f, 0.073f, 0.319f, 0.f},
+                              {64, 128, 2, 5.1f, 0.105f, 0.048f, 0.207f, 0.f},
+                              {32, 64, 2, 5.6f, 0.029f, 0.037f, 0.123f, 3.5f}};
 // K slices: the reduction's launch, and a byte of partials (in the same fit).
 constexpr float kSliceLaunch = 2.3f, kSliceByte = 2.8e-7f;
 
@@ -475,14 +477,20 @@ struct Mx4Plan {
 float tiles_time(const Mx4Cost &c, float tiles, float steps) {
   const float q = tiles / static_cast<float>(device_cus()), most = static_cast<float>(c.most);
   const float rounds = static_cast<float>(static_cast<int>(q / most)), rest = q - rounds * most;
-  return c.t0 + steps * (rounds * c.full + (rest > 0.f ? c.lone + c.shared * rest : 0.f));
+  return c.t0 + steps * (rounds * c.full + (rest > 0.f ? c.lone + c.shared * rest : 0.f)) +
+         c.again * std::max(0.f, rest > 0.f ? rounds : rounds - 1.f);
 }
 
 // The tile, and for few tiles the K slices, with the least time by the
 // measured costs; a slice's partials cost another launch and their traffic.
 // Up to 16 rows the streaming kernel, which reads each weight once with no
-// row padding beyond 16 (m = 13, n = 18944, k = 3584: 13.6 us against 15.0 on
-// 32 x 64 tiles; m = 32: 20.4 against 16.8).  A grouped product's row tiles
+// row padding beyond 16 (m = 13, n = 18944, k = 3584: 10.2 us against 14.8 on
+// 32 x 64 tiles), and up to 32 while its two row slabs still find a CU for
+// every five column tiles (m = 32, n = k = 4096: 7.3 against 9.1, MX4
+// activations 5.1 against 7.3; n = 11264 13.5 against 11.4), with 16-bit
+// activations up to k = 8192 (n = 4096: 11.5 against 11.9 with K slices;
+// k = 18944, n = 3584: 23.0 against 18.4; MX4 activations 14.7 against 15.1).
+// A grouped product's row tiles
 // are not known to the host: it reckons with half a tile too many for every
 // expert (on 27 sizes of 12 to 256 rows an expert, 8 to 128 experts, the tile
 // so picked is within 1 % of the best on average, 16 % at worst) and takes no
@@ -507,7 +515,8 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   const int windows = mx4_scale_windows(K);
   if (ov.mx4_tile >= 0 && !(grouped && ov.mx4_tile == kMx4T32)) {
     pl.tile = ov.mx4_tile;
-  } else if (M > (grouped ? std::max<int64_t>(7 * int64_t(E), std::min<int64_t>(12 * int64_t(E), 96)) : 16)) {
+  } else if (M > (grouped ? std::max<int64_t>(7 * int64_t(E), std::min<int64_t>(12 * int64_t(E), 96))
+                          : N / 16 * 2 <= 5 * device_cus() && (a4 || K <= 8192) ? 32 : 16)) {
     float best = 0.f;
     for (int i = 0; i < (grouped ? 4 : 5); ++i) {
       const int64_t cols = (N + cost[i].bn - 1) / cost[i].bn;
