@@ -102,7 +102,7 @@ __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4])
 // 32 and 64 were slower than the tiles (every wave reads its activations out
 // of L2 by itself).  Measured: M = 1, N = 131072, K = 2048 (142.6 MB) 23.6 us,
 // 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 9.8 us; MX4 activations of 8
-// rows there 8.5; 48 rows over 64 experts of 2816 x 2048 18.9.
+// rows there 7.5; 48 rows over 64 experts of 2816 x 2048 18.6.
 // ---------------------------------------------------------------------------
 // 4 x 4 transpose over the four 16-lane rows of a wave: a[t] of lane row j and
 // a[j] of lane row t trade places.
@@ -438,7 +438,7 @@ constexpr int kT32Groups = 4;
 // the workgroups take from each other).  Fitted to 2868 timings on MI355X, 17
 // to 4096 rows and eight weight shapes of 512 x 2048 to 18944 x 3584, each
 // tile and slice count forced (residual 6 to 8 %); the tile it picks is within
-// 3 % of the best one on average, 29 % at worst.
+// 4 % of the best one on average, 37 % at worst (2048 x 512, k = 2048).
 // 32 x 64 tiles, one a workgroup, pay a start (again) for every further round
 // (32 x 131072 x 2048: 48 us against 35.6 on 64 x 128 tiles).
 struct Mx4Cost {
