@@ -386,6 +386,7 @@ qg_status qunrepack_mx4(const uint8_t *codes_tiled, const uint8_t *scales_tiled,
  *   Tile multiples: n % 16 == 0, k % 128 == 0; m and rows any value >= 0.
  *   Alignment: A, B, C 16 bytes, scales and offsets 4, bias 2.
  *   A NaN scale makes NaN of the outputs that read it.
+ *   C and the workspace must not overlap the inputs or each other.
  *   workspace: optional device scratch, 256-byte aligned.  With at least
  *   qgemm_mx4_workspace_size(m, n, k, act_bits) bytes (act_bits 16 or 4; > 0
  *   for problems with few tiles) K slices write fp32 partials [slices, m, n]

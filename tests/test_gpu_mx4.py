@@ -289,6 +289,44 @@ def test_every_kernel_exact_sums(m, n, k, kernel):
         same(got, ref.rne(c + bias, dtype))
 
 
+@pytest.mark.parametrize("act", ["a16", "a4"])
+def test_several_tiles_a_workgroup_exact_sums(act):
+    """More tiles than workgroups run at a time, of every size: each walks
+    over tile borders, the last rows and columns ragged."""
+    m, n, k = 4100, 4368, 640
+    codes, scales, ac, asc, a, w, bias, c = exact_case(np.random.default_rng(m), m, n, k, act)
+    B, bias_d = qg.repack_mx4(dev(ref.pack(codes)), dev(scales)), dev(bias).to(BF)
+    for kernel in KERNELS[1:]:
+        qg.set_override(mx4_tile=kernel)
+        if act == "a16":
+            same(qg.gemm_mx4a16(torch.from_numpy(a).to(BF).cuda(), *B, bias=bias_d), ref.rne(c + bias, BF))
+        else:
+            A = qg.repack_mx4(dev(ref.pack(ac)), dev(asc))
+            for dtype in (HF, SF):
+                same(qg.gemm_mx4a4(*A, *B, m=m, bias=bias_d, out_dtype=dtype), ref.rne(c + bias, dtype))
+
+
+@pytest.mark.parametrize("m,k", [(1, 128), (13, 640), (20, 384)])
+@pytest.mark.parametrize("rounds", [1, 2, 3, 4, 5, 6, 7, 9, 11])
+def test_streaming_every_width_exact_sums(rounds, m, k):
+    """Column tiles for so many rounds of one per CU, so each number of column
+    tiles a workgroup takes, the last workgroup's not all there."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    n = 16 * (cus * rounds // ((m + 15) // 16) - 1)
+    qg.set_override(mx4_tile="stream")
+    rng = np.random.default_rng(rounds * m)
+    codes, scales, _, _, a, w, bias, c = exact_case(rng, m, n, k, "a16")
+    B = qg.repack_mx4(dev(ref.pack(codes)), dev(scales))
+    for dtype in (BF, HF):
+        got = qg.gemm_mx4a16(torch.from_numpy(a).to(dtype).cuda(), *B, bias=dev(bias).to(BF))
+        same(got, ref.rne(c + bias, dtype))
+    codes, scales, ac, asc, a, w, bias, c = exact_case(rng, m, n, k, "a4")
+    B = qg.repack_mx4(dev(ref.pack(codes)), dev(scales))
+    for dtype in (BF, HF, SF):
+        got = qg.gemm_mx4a4(*tiled(ac, asc), *B, m=m, bias=dev(bias).to(HF), out_dtype=dtype)
+        same(got, ref.rne(c + bias, dtype))
+
+
 @pytest.mark.parametrize("kernel", KERNELS[1:])
 @pytest.mark.parametrize("m,n,k,slices", [(1, 16, 1024, 2), (70, 272, 1664, 4), (300, 144, 3584, 3)])
 def test_k_slices_exact_sums(m, n, k, slices, kernel):
@@ -365,6 +403,16 @@ def test_grouped_many_experts(rows, kernel):
     out = torch.full((a.shape[0], 144), 9.0, dtype=BF, device="cuda")
     qg.gemm_mx4a16_grouped(torch.from_numpy(a).to(BF).cuda(), off, B, S, dev(bias).to(BF), out=out)
     same(out, ref.rne(c, BF))
+
+
+def test_grouped_several_tiles_a_workgroup():
+    n, k = 4368, 640
+    a, off, B, S, bias, c = grouped_case(np.random.default_rng(8), [700, 0, 1500, 3, 900, 400], n, k, 2, 3)
+    A = torch.from_numpy(a).to(BF).cuda()
+    for kernel in KERNELS[1:5]:
+        qg.set_override(mx4_tile=kernel)
+        out = torch.full((a.shape[0], n), 9.0, dtype=BF, device="cuda")
+        same(qg.gemm_mx4a16_grouped(A, off, B, S, dev(bias).to(BF), out=out), ref.rne(c, BF))
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
