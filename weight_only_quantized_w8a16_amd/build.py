@@ -25,8 +25,10 @@ HOST_SOURCES = ["api.cpp", "override.cpp"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function"]
 # Packed fp32 VALU ops disabled: plain float code must not be turned into
 # v_pk_{add,mul,fma}_f32.
+# A launch bound or an unrolling that the compiler cannot keep is an error:
+# host code and comments reckon with what the kernels ask for.
 DEVICE_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",
-                "-packed-fp32-ops", "-munsafe-fp-atomics"]
+                "-packed-fp32-ops", "-munsafe-fp-atomics", "-Werror=pass-failed"]
 
 
 def _compile(src: str) -> str:

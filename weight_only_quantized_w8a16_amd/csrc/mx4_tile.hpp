@@ -131,8 +131,12 @@ struct Mx4Engine16 {
   static constexpr int B_LOADS = BN / 32;              // 1 KiB code loads (32 channels) per step
   static constexpr int B_DMA = (B_LOADS + NW - 1) / NW;
   static constexpr int STAGE_A = BM * 128, STAGE = STAGE_A + BN * 32;
-  // Waves a SIMD holds: two with 128 accumulators a lane, four with fewer.
-  static constexpr int WAVES = WTM * WTN > 64 * 64 ? 2 : 4;
+  // Waves a SIMD is bound to hold: a lane's registers (91 to 256 of a SIMD's
+  // 512, 32 to 128 of them accumulators) let every tile have two.  A bound of
+  // four, which they cannot meet, put accumulators of the smaller tiles into
+  // the other half of the register file: 512 x 18944 x 3584 on 128 x 128 82.0
+  // us against 81.2, MX4 activations 34.2 against 33.7.
+  static constexpr int WAVES = 2;
   static constexpr int LOADS = A_DMA + B_DMA, SCALE_LOADS = 2 * TN;
   static_assert(WTM % 32 == 0 && WTN % 32 == 0 && A_DMA >= 2 && A_DMA % 2 == 0, "tile shape");
   static_assert(B_LOADS % NW == 0 || NW % B_LOADS == 0, "code loads shared out evenly");
@@ -407,8 +411,7 @@ struct Mx4Engine4 {
   static constexpr int A_BLK = BM / 16, B_BLK = BN / 16;   // code blocks per step
   static constexpr int A_DMA = (A_BLK + NW - 1) / NW, B_DMA = (B_BLK + NW - 1) / NW;
   static constexpr int STAGE_A = BM * 64, STAGE = STAGE_A + BN * 64;
-  // Waves a SIMD holds: two with 128 accumulators a lane, four with fewer.
-  static constexpr int WAVES = WTM * WTN > 64 * 64 ? 2 : 4;
+  static constexpr int WAVES = 2;   // a SIMD, as above
   static constexpr int LOADS = A_DMA + B_DMA, SCALE_LOADS = TM + TN;
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "tile shape");
   static_assert((A_BLK % NW == 0 || NW % A_BLK == 0) && (B_BLK % NW == 0 || NW % B_BLK == 0),
