@@ -42,6 +42,10 @@ def _compile(src: str) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{res.stderr}")
+    # Warnings, but for the host pass's about the device's feature.
+    said = [ln for ln in res.stderr.splitlines() if ln.strip() and not ln.startswith("'-packed-fp32-ops'")]
+    if said:
+        print(f"hipcc on {src}:", *said, sep="\n", file=sys.stderr, flush=True)
     return obj
 
 
