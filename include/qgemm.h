@@ -352,6 +352,8 @@ qg_status qembed_w8(const int32_t *ids, int tokens, const int8_t *table, int lay
  * qrepack_mx4 / qunrepack_mx4: portable -> tiled and back, exact inverses.
  *   rows == 0 or k == 0: no-op.  Alignment: X, out and codes 16 bytes,
  *   scales 4 (tiled) or 1 (portable).  Inputs and outputs must not overlap.
+ *   QG_ERR_UNSUPPORTED: k off its multiple, rows above 2^31 - 16, tiled
+ *   k above 2^31 - 512.
  * ---------------------------------------------------------------------- */
 qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k, int layout,
                         qg_dtype x_dtype, void *stream);

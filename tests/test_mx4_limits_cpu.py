@@ -1,0 +1,23 @@
+"""MX4 operators at the ends of their sizes: refused on the host, before a
+launch (no GPU; the addresses are stand-ins)."""
+import pytest
+
+import weight_only_quantized_w8a16_amd as qg
+
+UNSUP = 7
+FAKE = 0x100000          # 16-byte-aligned stand-in address; never dereferenced
+BF16, TILED = 1, 1
+
+
+def conversions(rows, k):
+    L = qg.lib()
+    return {"quantize": L.qquantize_mx4(FAKE, FAKE, FAKE, rows, k, TILED, BF16, None),
+            "dequant": L.qdequant_mx4(FAKE, FAKE, FAKE, rows, k, TILED, BF16, None),
+            "repack": L.qrepack_mx4(FAKE, FAKE, FAKE, FAKE, rows, k, None),
+            "unrepack": L.qunrepack_mx4(FAKE, FAKE, FAKE, FAKE, rows, k, None)}
+
+
+@pytest.mark.parametrize("k", [2 ** 31 - 128, 2 ** 31 - 256, 2 ** 31 - 384])
+def test_tiled_conversions_refuse_k_whose_windows_pass_32_bits(k):
+    # k + 511, of which the 512-k windows are counted, is past 2^31 - 1
+    assert set(conversions(1, k).values()) == {UNSUP}

@@ -326,7 +326,8 @@ static qg_status mx4_layout_checks(const void *codes, const void *scales, const 
                                    int k, int layout) {
   if (layout != QG_LAYOUT_PORTABLE && layout != QG_LAYOUT_TILED) return QG_ERR_MODE;
   const bool tiled = layout == QG_LAYOUT_TILED;
-  if (k % (tiled ? 128 : 32) != 0 || rows > INT32_MAX - 15) return QG_ERR_UNSUPPORTED;
+  if (k % (tiled ? 128 : 32) != 0 || rows > INT32_MAX - 15 || (tiled && k > INT32_MAX - 511))
+    return QG_ERR_UNSUPPORTED;   // padded rows, and 512-k windows, counted in 32 bits
   if (!aligned(codes, 16) || (tiled && !aligned(scales, 4)) || (x && !aligned(x, 16)))
     return QG_ERR_ALIGN;
   return QG_OK;
