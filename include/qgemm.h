@@ -353,7 +353,8 @@ qg_status qembed_w8(const int32_t *ids, int tokens, const int8_t *table, int lay
  *   rows == 0 or k == 0: no-op.  Alignment: X, out and codes 16 bytes,
  *   scales 4 (tiled) or 1 (portable).  Inputs and outputs must not overlap.
  *   QG_ERR_UNSUPPORTED: k off its multiple, rows above 2^31 - 16, tiled
- *   k above 2^31 - 512.
+ *   k above 2^31 - 512, a tiled matrix of 2^24 and more pieces of 16 rows x
+ *   512 k (one launch's).
  * ---------------------------------------------------------------------- */
 qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k, int layout,
                         qg_dtype x_dtype, void *stream);
@@ -386,6 +387,9 @@ qg_status qunrepack_mx4(const uint8_t *codes_tiled, const uint8_t *scales_tiled,
  *   experts  1 .. 65536
  * Common: bias in bias_dtype (QG_BF16 or QG_FP16), or NULL with QG_NONE.
  *   Tile multiples: n % 16 == 0, k % 128 == 0; m and rows any value >= 0.
+ *   QG_ERR_UNSUPPORTED also for m, rows or n above 2^31 - 256, k above
+ *   2^31 - 512, and results of more tiles than one launch covers (from n =
+ *   2^29 on, or 2^43 values).
  *   Alignment: A, B, C 16 bytes, scales and offsets 4, bias 2.
  *   A NaN scale makes NaN of the outputs that read it.
  *   C and the workspace must not overlap the inputs or each other.

@@ -21,3 +21,18 @@ def conversions(rows, k):
 def test_tiled_conversions_refuse_k_whose_windows_pass_32_bits(k):
     # k + 511, of which the 512-k windows are counted, is past 2^31 - 1
     assert set(conversions(1, k).values()) == {UNSUP}
+
+
+@pytest.mark.parametrize("rows,k", [(2 ** 28, 128), (2 ** 28 + 1, 512), (2 ** 24, 16 * 512)])
+def test_tiled_conversions_of_more_pieces_than_a_launch_has(rows, k):
+    assert (rows + 15) // 16 * ((k + 511) // 512) >= 2 ** 24
+    assert set(conversions(rows, k).values()) == {UNSUP}
+
+
+@pytest.mark.parametrize("k", [1024, 8192])
+def test_products_wider_than_a_launch(k):
+    n = 2 ** 30
+    L = qg.lib()
+    assert L.qgemm_mx4a16(FAKE, FAKE, FAKE, None, FAKE, 4, n, k, BF16, 0, None, 0, None) == UNSUP
+    assert L.qgemm_mx4a4(FAKE, FAKE, FAKE, FAKE, None, FAKE, 4, n, k, BF16, 0, None, 0, None) == UNSUP
+    assert L.qgemm_mx4a16_grouped(FAKE, FAKE, FAKE, FAKE, None, FAKE, 4, n, k, 2, BF16, 0, None) == UNSUP

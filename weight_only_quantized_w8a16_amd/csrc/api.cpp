@@ -333,6 +333,11 @@ static qg_status mx4_layout_checks(const void *codes, const void *scales, const 
   return QG_OK;
 }
 
+// hipErrorNotSupported: sizes past what one launch covers.
+static qg_status mx4_status(hipError_t e) {
+  return e == hipErrorNotSupported ? QG_ERR_UNSUPPORTED : hip_status(e);
+}
+
 qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k, int layout,
                         qg_dtype x_dt, void *stream) {
   if (rows < 0 || k < 0) return QG_ERR_SHAPE;
@@ -341,7 +346,7 @@ qg_status qquantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows
   if (!act_ok(x_dt) && x_dt != QG_FP32) return QG_ERR_DTYPE;
   const qg_status st = mx4_layout_checks(codes, scales, X, rows, k, layout);
   if (st != QG_OK) return st;
-  return hip_status(qg::launch_quantize_mx4(X, codes, scales, rows, k, layout == QG_LAYOUT_TILED,
+  return mx4_status(qg::launch_quantize_mx4(X, codes, scales, rows, k, layout == QG_LAYOUT_TILED,
                                             static_cast<int>(x_dt), as_stream(stream)));
 }
 
@@ -353,7 +358,7 @@ qg_status qdequant_mx4(const uint8_t *codes, const uint8_t *scales, void *out, i
   if (!act_ok(out_dt) && out_dt != QG_FP32) return QG_ERR_DTYPE;
   const qg_status st = mx4_layout_checks(codes, scales, out, rows, k, layout);
   if (st != QG_OK) return st;
-  return hip_status(qg::launch_dequant_mx4(codes, scales, out, rows, k, layout == QG_LAYOUT_TILED,
+  return mx4_status(qg::launch_dequant_mx4(codes, scales, out, rows, k, layout == QG_LAYOUT_TILED,
                                            static_cast<int>(out_dt), as_stream(stream)));
 }
 
@@ -369,14 +374,14 @@ qg_status qrepack_mx4(const uint8_t *codes, const uint8_t *scales, uint8_t *code
                       uint8_t *scales_t, int rows, int k, void *stream) {
   qg_status st = mx4_repack_checks(codes, scales, codes_t, scales_t, rows, k);
   if (st != QG_OK || rows == 0 || k == 0) return st;
-  return hip_status(qg::launch_repack_mx4(codes, scales, codes_t, scales_t, rows, k, as_stream(stream)));
+  return mx4_status(qg::launch_repack_mx4(codes, scales, codes_t, scales_t, rows, k, as_stream(stream)));
 }
 
 qg_status qunrepack_mx4(const uint8_t *codes_t, const uint8_t *scales_t, uint8_t *codes,
                         uint8_t *scales, int rows, int k, void *stream) {
   qg_status st = mx4_repack_checks(codes, scales, codes_t, scales_t, rows, k);
   if (st != QG_OK || rows == 0 || k == 0) return st;
-  return hip_status(qg::launch_unrepack_mx4(codes_t, scales_t, codes, scales, rows, k, as_stream(stream)));
+  return mx4_status(qg::launch_unrepack_mx4(codes_t, scales_t, codes, scales, rows, k, as_stream(stream)));
 }
 
 size_t qgemm_mx4_workspace_size(int m, int n, int k, int act_bits) {
@@ -408,7 +413,7 @@ static qg_status mx4_gemm(const void *A, const uint8_t *AS, const int32_t *offse
   const qg::Mx4Args a{A, AS, B, BS, static_cast<const uint16_t *>(bias), C, m, n, k,
                       a4 ? qg::kMX4 : static_cast<int>(out), static_cast<int>(out), static_cast<int>(bias_dt), offsets,
                       grouped ? experts : 0, workspace, workspace ? ws_bytes : 0};
-  return hip_status(qg::launch_mx4_gemm(a, as_stream(stream)));
+  return mx4_status(qg::launch_mx4_gemm(a, as_stream(stream)));
 }
 
 qg_status qgemm_mx4a16(const void *A, const uint8_t *B, const uint8_t *BS, const void *bias, void *C,

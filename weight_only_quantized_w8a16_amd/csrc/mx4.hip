@@ -223,7 +223,7 @@ hipError_t quantize_dt(const void *X, uint8_t *codes, uint8_t *scales, int rows,
                        hipStream_t s) {
   if (tiled) {
     const size_t grid = tiled_grid(rows, k);
-    if (grid > kMostGroups) return hipErrorInvalidValue;
+    if (grid > kMostGroups) return hipErrorNotSupported;
     hipLaunchKernelGGL(k_mx4_quantize_tiled<DT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, X,
                        reinterpret_cast<uint32_t *>(codes), reinterpret_cast<uint32_t *>(scales), rows, k);
   } else {
@@ -239,7 +239,7 @@ hipError_t dequant_dt(const uint8_t *codes, const uint8_t *scales, void *out, in
                       hipStream_t s) {
   if (tiled) {
     const size_t grid = tiled_grid(rows, k);
-    if (grid > kMostGroups) return hipErrorInvalidValue;
+    if (grid > kMostGroups) return hipErrorNotSupported;
     hipLaunchKernelGGL(k_mx4_dequant_tiled<DT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s,
                        reinterpret_cast<const uint32_t *>(codes), reinterpret_cast<const uint32_t *>(scales),
                        out, rows, k);
@@ -255,7 +255,7 @@ template <bool TO_TILED>
 hipError_t relayout(const uint8_t *src_c, const uint8_t *src_s, uint8_t *dst_c, uint8_t *dst_s, int rows,
                     int k, hipStream_t s) {
   const size_t grid = tiled_grid(rows, k);
-  if (grid > kMostGroups) return hipErrorInvalidValue;
+  if (grid > kMostGroups) return hipErrorNotSupported;
   hipLaunchKernelGGL(k_mx4_relayout<TO_TILED>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, src_c,
                      src_s, dst_c, dst_s, rows, k);
   return hipGetLastError();

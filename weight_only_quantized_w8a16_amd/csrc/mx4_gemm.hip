@@ -367,7 +367,7 @@ hipError_t run_stream_as(const Mx4Problem &p, long slabs, hipStream_t s) {
   const int nb = p.K >> 7, waves = nb < 8 ? nb : 8;
   const size_t lds = static_cast<size_t>(waves) * NT * 256 * sizeof(float);
   const unsigned cols = static_cast<unsigned>(((p.N >> 4) + NT - 1) / NT);
-  if (static_cast<uint64_t>(cols) * 64 * waves > UINT32_MAX) return hipErrorInvalidValue;
+  if (static_cast<uint64_t>(cols) * 64 * waves > UINT32_MAX) return hipErrorNotSupported;
   for (long s0 = 0; s0 < slabs; s0 += kMaxSlabs) {
     const unsigned ny = static_cast<unsigned>(std::min<long>(slabs - s0, kMaxSlabs));
     hipLaunchKernelGGL((k_mx4_stream<ACT, OUT, NT, GROUPED, DEPTH>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
@@ -571,7 +571,7 @@ hipError_t run_tiles(const Mx4Problem &p, hipStream_t s) {
   // A grouped product has at most one partial row tile per expert with rows.
   const int64_t tm = GROUPED ? p.M / Eng::BM + std::min(p.E, p.M) : (p.M + Eng::BM - 1) / Eng::BM;
   const int64_t items = tm * tn * p.slices;
-  if (items > INT32_MAX / 2) return hipErrorInvalidValue;
+  if (items > INT32_MAX / 2) return hipErrorNotSupported;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, device_cus() * groups_per_cu<Eng>()));
   if constexpr (GROUPED) {
     hipLaunchKernelGGL((k_mx4_tiles<Eng, Mx4Out<OUT, false>, Mx4GroupWork<Eng>>), dim3(grid), dim3(Eng::NTHR), 0, s, p);
@@ -588,7 +588,7 @@ template <class Eng, int KW, int OUT>
 hipError_t run_one_tile(const Mx4Problem &p, hipStream_t s) {
   const int64_t tn = (p.N + Eng::BN - 1) / Eng::BN, tm = (p.M + Eng::BM - 1) / Eng::BM;
   const int64_t items = tm * tn * p.slices;
-  if (items * Eng::NTHR * KW > UINT32_MAX) return hipErrorInvalidValue;
+  if (items * Eng::NTHR * KW > UINT32_MAX) return hipErrorNotSupported;
   const dim3 grid(static_cast<unsigned>(items)), block(Eng::NTHR * KW);
   if (p.slices > 1) {
     hipLaunchKernelGGL((k_mx4_one_tile<Eng, KW, Mx4Out<OUT, true>>), grid, block, 0, s, p);

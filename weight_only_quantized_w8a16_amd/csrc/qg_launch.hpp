@@ -181,7 +181,8 @@ hipError_t launch_embed(const EmbedArgs &a, hipStream_t s);
 
 namespace qg {
 
-// Microscaled 4-bit floats (MX4).
+// Microscaled 4-bit floats (MX4).  hipErrorNotSupported: the sizes need more
+// threads than a launch has (2^32 - 1); nothing is enqueued.
 hipError_t launch_quantize_mx4(const void *X, uint8_t *codes, uint8_t *scales, int rows, int k,
                                int tiled, int x_dt, hipStream_t s);
 hipError_t launch_dequant_mx4(const uint8_t *codes, const uint8_t *scales, void *out, int rows,
