@@ -513,7 +513,11 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
     return pl;
   const Mx4Cost *cost = a4 ? kCost4 : kCost16;
   const int windows = mx4_scale_windows(K);
-  if (ov.mx4_tile >= 0 && !(grouped && ov.mx4_tile == kMx4T32)) {
+  // A forced 32 x 64 tile fits a dense product whose tiles (and slices of them)
+  // one launch covers, a workgroup of 128 * kT32Groups threads each.
+  const int64_t t32 = static_cast<int64_t>((M + 31) / 32) * ((N + 63) / 64) * std::max(1, std::min(ov.mx4_split, windows));
+  const bool t32_fits = !grouped && t32 * 128 * kT32Groups <= UINT32_MAX;
+  if (ov.mx4_tile >= 0 && (ov.mx4_tile != kMx4T32 || t32_fits)) {
     pl.tile = ov.mx4_tile;
   } else if (M > (grouped ? std::max<int64_t>(7 * int64_t(E), std::min<int64_t>(12 * int64_t(E), 96))
                           : N / 16 * 2 <= 5 * device_cus() && (a4 || K <= 8192) ? 32 : 16)) {
