@@ -36,3 +36,12 @@ def test_products_wider_than_a_launch(k):
     assert L.qgemm_mx4a16(FAKE, FAKE, FAKE, None, FAKE, 4, n, k, BF16, 0, None, 0, None) == UNSUP
     assert L.qgemm_mx4a4(FAKE, FAKE, FAKE, FAKE, None, FAKE, 4, n, k, BF16, 0, None, 0, None) == UNSUP
     assert L.qgemm_mx4a16_grouped(FAKE, FAKE, FAKE, FAKE, None, FAKE, 4, n, k, 2, BF16, 0, None) == UNSUP
+
+
+@pytest.mark.parametrize("m,n,k", [(2 ** 32 + 64, 256, 4096), (64, 2 ** 32 + 256, 4096), (64, 256, 2 ** 32 + 4096),
+                                   (-2 ** 32 + 64, 256, 4096)])
+def test_workspace_size_of_sizes_past_32_bits(m, n, k):
+    # no problem the library takes; as 32-bit integers they would wrap into one
+    qg.set_override(mx4_tile="T64", mx4_split=4)
+    assert qg.mx4_workspace_size(64, 256, 4096, 16) > 0
+    assert qg.mx4_workspace_size(m, n, k, 16) == 0

@@ -623,6 +623,8 @@ def unrepack_mx4(codes: torch.Tensor, scales: torch.Tensor, rows: Optional[int] 
 
 
 def mx4_workspace_size(m: int, n: int, k: int, act_bits: int) -> int:
+    if min(m, n, k) < 0 or max(m, n, k) > _MX4_MOST:
+        return 0   # no problem the library takes
     return int(lib().qgemm_mx4_workspace_size(m, n, k, act_bits))
 
 
