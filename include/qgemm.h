@@ -347,7 +347,7 @@ qg_status qembed_w8(const int32_t *ids, int tokens, const int8_t *table, int lay
  * qdequant_mx4: codes and scales -> out [rows, k] in out_dtype (QG_BF16,
  * QG_FP16 or QG_FP32): the value rounded to nearest even (bf16 and fp32 hold
  * every value but those of 2^128 and above, which round to infinity; fp16
- * also rounds below 2^-23).  rows counts the valid rows; padding rows of the
+ * rounds below 2^-23, and to infinity from 65520 on).  rows counts the valid rows; padding rows of the
  * tiled layout are not written to out.
  * qrepack_mx4 / qunrepack_mx4: portable -> tiled and back, exact inverses.
  *   rows == 0 or k == 0: no-op.  Alignment: X, out and codes 16 bytes,
@@ -369,12 +369,15 @@ qg_status qunrepack_mx4(const uint8_t *codes_tiled, const uint8_t *scales_tiled,
  * qgemm_mx4a16:  C[m, n] = sum_k A[m, k] * W[n, k] (+ bias[n])
  *   A        device [m, k] in act_dtype (QG_BF16 or QG_FP16)
  *   C        device [m, n] in act_dtype; written, never read
- *   W is value(B) in act_dtype: exact in bf16; in fp16 rounded as by
- *   qdequant_mx4 (exact for values of 2^-23 and above, below 65520).
+ *   W is value(B) in act_dtype, as by qdequant_mx4: in bf16 exact, subnormal
+ *   values too, below 2^128; in fp16 exact from 2^-23 to 65519, rounded below,
+ *   and infinite from 65520 on (then NaN where the activation is 0).  Blocks
+ *   with larger values need bf16 activations.
  * qgemm_mx4a4:  C[m, n] = sum_k value(A)[m, k] * W[n, k] (+ bias[n])
  *   A        codes and scales of the activations, tiled, m rows (padded to 16)
  *   C        device [m, n] in out_dtype (QG_BF16, QG_FP16 or QG_FP32)
- *   The products are exact, also across scales.
+ *   The products are exact in fp32, also across scales; one outside its range
+ *   (subnormal numbers belong to it) rounds to zero or infinity.
  * qgemm_mx4a16_grouped:  rows offsets[e] .. offsets[e+1] - 1 of A times
  *   expert e's weight (rows sorted by expert, any number of rows each):
  *       C[r, n] = sum_k A[r, k] * W_e[n, k] (+ bias[e, n])

@@ -645,7 +645,9 @@ def gemm_mx4a16(A: torch.Tensor, B_tiled: torch.Tensor, B_scales: torch.Tensor,
                 bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C = A . value(B)^T (+ bias); A [..., k] bf16/fp16, B tiled MX4 [n, k]
-    (repack_mx4, or quantize_mx4 with tiled=True)."""
+    (repack_mx4, or quantize_mx4 with tiled=True).  The weight is widened to
+    A's dtype: in fp16 its values below 2^-23 are rounded, and those from 65520
+    on are infinite."""
     f = "qgemm_mx4a16"
     if A.dtype not in _ACT or A.dim() < 1:
         raise QGemmError(f, _DTYPE, f"A must be bf16 or fp16 (got {A.dtype})")

@@ -2,7 +2,8 @@
 //   C[m, n] = sum_k A[m, k] * value(B)[n, k] (+ bias[n]),
 // A in 16 bits or MX4, dense or grouped by expert (include/qgemm.h).  Sums are
 // fp32; the one rounding is the store to C's type (and in fp16 that of a
-// weight below 2^-23 or from 65520 on, as the conversion's).
+// weight below 2^-23 or, to infinity, from 65520 on, as the conversion's).
+// Subnormal operands, products and sums are kept.
 //
 // Every block of 32 weights has a power-of-two scale, so a scaled weight is
 // exact in bf16 and the conversion instructions apply the scale while they
