@@ -1,11 +1,12 @@
 // mx4.hip -- conversions of the microscaled 4-bit format (MX4): quantize,
 // read back, and the change between the portable and the tiled layout.  All
 // of them are bound by HBM (the smallest by a launch): a value is read or
-// written once and everything else happens in registers.  Measured in bf16:
-// 13312 x 2048 (54.5 MB of values, 14.5 MB of codes and scales) portable
-// quantize 11.6 us, read back 11.9 us (5.9 TB/s), tiled 12.1 and 11.6;
-// 4096 x 18944 28.9 and 29.9 us (6.7 TB/s); 16 x 2048 2.3 and 2.2 us.
-// The layout change of 13312 x 2048 takes 7.7 us.
+// written once and everything else happens in registers.  Measured in bf16,
+// back to back on inputs in turn (500 MB, or 40 inputs where those are less
+// and stay in the caches): 13312 x 2048 (54.5 MB of values, 14.5 MB of codes
+// and scales) portable quantize 11.6 us, read back 11.9 us (5.9 TB/s), tiled
+// 12.1 and 11.6; 4096 x 18944 28.9 and 29.9 us (6.7 TB/s); 16 x 2048 2.3 and
+// 2.2 us.  The layout change of 13312 x 2048 takes 7.7 us.
 //
 // Four lanes share a 32-value block, eight values each (16 bytes of a 16-bit
 // row), so the block's largest magnitude is two quad exchanges away.  The
@@ -112,7 +113,9 @@ __global__ __launch_bounds__(kThreads) void k_mx4_quantize_tiled(const void *__r
   // All four blocks' loads first (past the end the last row and block again),
   // then their conversions: one memory latency instead of four.  8 x 3584 2.6
   // -> 2.3 us, 2048 x 640 3.6 -> 2.9, at 4096 x 3584 7.5 -> 7.8.  A thread per
-  // block and eighth (1024 a workgroup) gave 2.3, 2.6 and 8.6.
+  // block and eighth (1024 a workgroup) gave 2.3, 2.6 and 8.6.  (Values still in
+  // the caches, as an activation just written is; 8 x 3584 behind a product that
+  // reads 36 MB, so that they are not: 4.7.)
   float v[4][8];
 #pragma unroll
   for (int b = 0; b < 4; ++b)

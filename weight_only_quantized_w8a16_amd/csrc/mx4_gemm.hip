@@ -102,8 +102,9 @@ __device__ __forceinline__ void store4(void *C, size_t off, const float (&v)[4])
 // in LDS, so no wave waits for another's loads.  Bound by HBM; row blocks of
 // 32 and 64 were slower than the tiles (every wave reads its activations out
 // of L2 by itself).  Measured: M = 1, N = 131072, K = 2048 (142.6 MB) 23.6 us,
-// 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 9.8 us; MX4 activations of 8
-// rows there 7.5; 48 rows over 64 experts of 2816 x 2048 18.6.
+// 6.0 TB/s; M = 13, N = 18944, K = 3584 (36 MB) 9.7 us; MX4 activations of 8
+// rows there 7.6; 48 rows over 64 experts of 2816 x 2048 19.5 (each launch by
+// itself; back to back 9.9, 9.1 and 20.0).
 // ---------------------------------------------------------------------------
 // 4 x 4 transpose over the four 16-lane rows of a wave: a[t] of lane row j and
 // a[j] of lane row t trade places.
@@ -314,9 +315,10 @@ struct Mx4GroupWork {
   }
 };
 
-// bf16 activations, 2048 x 13312 x 2048: 90.5 us (1.23 PFLOP/s) on 256 x 256
-// tiles, 12288 rows over 64 experts of 2816 x 2048 153 us (0.93) on 128 x 256;
-// MX4 activations, 4096 x 18944 x 3584: 144 to 150 us (3.7 to 3.9).
+// bf16 activations, 2048 x 13312 x 2048: 91 to 97 us (1.15 to 1.23 PFLOP/s) on
+// 256 x 256 tiles, 12288 rows over 64 experts of 2816 x 2048 153 to 158 us (0.90
+// to 0.93) on 128 x 256; MX4 activations, 4096 x 18944 x 3584: 144 to 150 us
+// (3.7 to 3.9).
 template <class Eng, class Out, class Work>
 __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem p) {
   __shared__ __attribute__((aligned(16))) char s0[Eng::STAGE];
@@ -329,7 +331,8 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_mx4_tiles(Mx4Problem 
   mx4_tiles<Eng, Out>(p, work, Mx4Lds{{s0, s1, s2, s3}, ep, bias});
 }
 
-// 100 x 3584 x 3584: 9.1 us, against 17.0 on 64 x 128 tiles in two K slices.
+// 100 x 3584 x 3584: 8.8 us back to back (9.5 by itself), against 16.5 on
+// 64 x 128 tiles in two K slices.
 template <class Eng, int KW, class Out>
 __global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
   __shared__ __attribute__((aligned(16))) float bias[Eng::NW * Eng::WTN];
@@ -344,7 +347,7 @@ __global__ __launch_bounds__(Eng::NTHR * KW) void k_mx4_one_tile(Mx4Problem p) {
 
 // K slices: C = RNE_out(the slices' partials summed in slice order + bias).
 // Bound by the partials' traffic out of MALL: three slices of 333 x 3584
-// (14.3 MB) 4.9 us.
+// (14.3 MB) 4.8 to 5.2 us.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_mx4_reduce(Mx4Problem p) {
   const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
@@ -485,8 +488,8 @@ float tiles_time(const Mx4Cost &c, float tiles, float steps) {
 // The tile, and for few tiles the K slices, with the least time by the
 // measured costs; a slice's partials cost another launch and their traffic.
 // Up to 16 rows the streaming kernel, which reads each weight once with no
-// row padding beyond 16 (m = 13, n = 18944, k = 3584: 10.2 us against 14.8 on
-// 32 x 64 tiles), and up to 32 while its two row slabs still find a CU for
+// row padding beyond 16 (bf16, back to back, m = 13, n = 18944, k = 3584: 10.2
+// us against 15.2 on 32 x 64 tiles), and up to 32 while its two row slabs still find a CU for
 // every five column tiles (m = 32, n = k = 4096: 7.3 against 9.1, MX4
 // activations 5.1 against 7.3; n = 11264 13.5 against 11.4), with 16-bit
 // activations up to k = 8192 (n = 4096: 11.5 against 11.9 with K slices;
@@ -495,8 +498,8 @@ float tiles_time(const Mx4Cost &c, float tiles, float steps) {
 // are not known to the host: it reckons with half a tile too many for every
 // expert (on 27 sizes of 12 to 256 rows an expert, 8 to 128 experts, the tile
 // so picked is within 1 % of the best on average, 16 % at worst) and takes no
-// 32-row tiles (2048 rows over 64 experts, n = 2816, k = 2048: 85.6 us against
-// 64.6 on 64-row ones).  It streams up to a mean of 7 rows an expert (64
+// 32-row tiles (2048 rows over 64 experts, n = 2816, k = 2048: 85.6 us, 64-row
+// ones 64.6 then and 56 to 61 now).  It streams up to a mean of 7 rows an expert (64
 // experts, n = 2048, k = 1408: 6 rows each 23.7 us against 26.3 on 64-row
 // tiles, 8 rows 26.8 against 25.9, 12 rows 31.9 against 27.6), or of 12 up to
 // 96 rows in all (8 experts, n = 3584, k = 2560: 8 rows each 12.6 against
@@ -507,7 +510,9 @@ Mx4Plan plan_mx4(int M, int N, int K, bool a4, bool grouped, int E) {
   // The tile kernels' buffer loads and stores have 32-bit offsets.  They span a
   // tile's rows of C (or of fp32 partials), an expert's scales, and with
   // 16-bit activations the tile's rows of A and its channels' codes; with MX4
-  // ones all codes of B (and of A: launch_mx4_gemm takes its rows in parts).
+  // ones all codes of B (and of A: launch_mx4_gemm takes its rows in parts).  So
+  // MX4 activations stream against 2^32 and more weights whatever their rows,
+  // every 16 rows reading all of them.
   const uint64_t lim = kMx4Span, windows64 = mx4_scale_windows(K) * uint64_t(256);
   if (uint64_t(256) * 4 * N >= lim || (N / 16) * windows64 >= lim || uint64_t(256) * K * 2 >= lim ||
       (a4 && uint64_t(N) * K / 2 >= lim))
