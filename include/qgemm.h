@@ -11,6 +11,7 @@
  *   int8, per channel: W[n, k] = q[n, k] * scale[n]
  *   int8, groupwise:   W[n, k] = q[n, k] * scale[n, k/g]   (no zero)
  *   MX4 (4-bit floats): W[n, k] = value(code[n, k]) * 2^(scale[n, k/32] - 127)
+ *   F8 (8-bit floats): W[n, k] = value(code[n, k]) * scale[n/128, k/128]
  *
  * Sources: "acext User Guide (v1.7)", 1.2.1 fpAintB GEMM (argument set: A,
  * B, scales, zero points, biases, C, m, n, k, group size, workspace, stream),
@@ -38,7 +39,8 @@
  *    tokens == 0) is a successful no-op that reads no pointer; k must be
  *    positive (repack and dequant also accept k == 0).  The first failed
  *    check decides the status, in the order: sizes, NULL pointers, dtypes,
- *    mode arguments (W8A8 quant mode, table layout, MoE normalization), group
+ *    mode arguments (W8A8 quant mode, table layout, MoE normalization, F8 block,
+ *    gate activation), group
  *    size, tile multiples, alignment, workspace.
  *  - Functions are reentrant; calls on different streams may overlap unless
  *    they share a workspace.
@@ -417,6 +419,139 @@ qg_status qgemm_mx4a16_grouped(const void *A, const int32_t *offsets, const uint
                                const uint8_t *B_scales, const void *bias, void *C, int rows, int n,
                                int k, int experts, qg_dtype act_dtype, qg_dtype bias_dtype,
                                void *stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled 8-bit floats (F8).  A code is an 8-bit float e4m3 (sign, 4
+ * exponent bits with bias 7, 3 mantissa bits; largest 448, 0x7F and 0xFF NaN,
+ * no infinities; the OCP 8-bit Floating Point Specification's E4M3), scales
+ * are fp32:  value = code * scale.  All code matrices are row-major with rows a
+ * multiple of 16 long; a block of 128 may be cut short by the matrix's end.
+ * With blocks(x) = ceil(x / 128), the scales of a [rows, k] matrix are
+ *     by rows (block 1):     float [blocks(k), rows], one per row and 128 k (the
+ *                            scales of one 128 k lie side by side)
+ *     by blocks (block 128): float [blocks(rows), blocks(k)], one per 128 x 128
+ * (The pages describe no 8-bit floating-point format; block-scaled checkpoints
+ * store their weights this way.)
+ *
+ * qquantize_f8: X [stack, rows, k] -> codes and scales of every matrix, and
+ * of its transpose.  A block's scale is 2^e with the smallest e >= -126 for which
+ * its largest magnitude / 2^e <= 448, and 1 for a block of zeros; a code is
+ * x / 2^e rounded to the nearest, ties to the even code, the sign kept (also of
+ * a zero).  A block holding a NaN or an infinity gets a NaN scale and codes 0: all
+ * its values read back as NaN.  Bit-exact by contract.
+ *   X        device [stack, rows, k], QG_BF16, QG_FP16 or QG_FP32
+ *   stack    matrices, >= 1; with block 1 only 1
+ *   block    1 or 128 (else QG_ERR_MODE)
+ *   Q, S     codes [stack, rows, k] and scales (per matrix), or both NULL
+ *   QT, ST   codes [stack, k, R] of the transposes, R = rows rounded up to 16,
+ *            padded with zeros' codes, and their scales (as a [k, R] matrix: by
+ *            rows [blocks(rows), k], by blocks [blocks(k), blocks(rows)]), or
+ *            both NULL.  By blocks they are the transposed Q and S; by rows the
+ *            128 values of a scale run along X's columns.
+ * qdequant_f8: codes and scales -> out [stack, rows, k] in out_dtype (QG_BF16,
+ * QG_FP16 or QG_FP32): code * scale in fp32, rounded to nearest even.  Any scales.
+ *   rows == 0 or k == 0: no-op.  Tile multiple: k % 16 == 0; rows any.
+ *   QG_ERR_UNSUPPORTED also for rows or k above 2^31 - 256, and sizes past one
+ *   launch (2^37 values).  Alignment: X, Q, QT and out 16 bytes, S and ST 4.
+ *   Inputs and outputs must not overlap.
+ * ---------------------------------------------------------------------- */
+qg_status qquantize_f8(const void *X, int stack, int rows, int k, qg_dtype x_dtype, int block,
+                       uint8_t *Q, float *S, uint8_t *QT, float *ST, void *stream);
+qg_status qdequant_f8(const uint8_t *Q, const float *S, void *out, int stack, int rows, int k,
+                      int block, qg_dtype out_dtype, void *stream);
+
+/* F8 products, fp32 accumulation, C = RNE_out(sum + bias).  Within an eight of
+ * consecutive k the matrix instruction cuts each product at 2^-13 of the largest
+ * one's power of two (towards zero); eights, blocks of 128 and their scales meet in
+ * fp32.  On normal operands that is 3e-5 of a result, an eighth of fp16's rounding.
+ * qgemm_f8:  C[m, n] = sum_k value(A)[m, k] * value(B)[n, k] (+ bias[n])
+ *   A        device codes [m, k], A_scales by rows [blocks(k), m]
+ *   B        device codes [n, k], B_scales by blocks (b_block 128) or by rows
+ *            (b_block 1; the weight's gradient needs it)
+ *   C        device [m, n] in out_dtype (QG_BF16, QG_FP16 or QG_FP32);
+ *            written, never read
+ * qgemm_f8_grouped:  rows offsets[e] .. offsets[e+1] - 1 of A times expert e's
+ *   weight (rows sorted by expert, any number of rows each):
+ *       C[r, n] = sum_k value(A)[r, k] * value(B[e])[n, k] (+ bias[e, n])
+ *   offsets  device int32 [experts + 1], as for qgemm_mx4a16_grouped: whatever
+ *            they hold, nothing outside the buffers is touched; rows of no
+ *            expert are left as they were.
+ *   B        [experts, n, k], B_scales [experts, blocks(n), blocks(k)], bias
+ *            [experts, n];  experts 1 .. 65536
+ * Common: bias in bias_dtype (QG_BF16 or QG_FP16), or NULL with QG_NONE.
+ *   The scales are any fp32 numbers; a product of an A and a B scale is rounded
+ *   to fp32 (so products below 2^-126 lose bits, and those past the largest
+ *   number are infinite).  A NaN code or scale makes NaN of the outputs that read it.
+ *   Tile multiples: n % 16 == 0, k % 16 == 0; m and rows any value >= 0.
+ *   QG_ERR_UNSUPPORTED also for m, rows, n or k above 2^31 - 256, and results of
+ *   more tiles than one launch covers.
+ *   Alignment: A, B, C 16 bytes, scales and offsets 4, bias 2.
+ *   C and the workspace must not overlap the inputs or each other.
+ *   workspace: optional device scratch, 256-byte aligned.  With at least
+ *   qgemm_f8_workspace_size(m, n, k, b_block) bytes (> 0 for problems with few
+ *   tiles) K slices write fp32 partials there and one more launch sums them in
+ *   slice order; with less (or NULL) the same call runs unsplit.  Calls that
+ *   share a workspace must not overlap. */
+size_t qgemm_f8_workspace_size(int m, int n, int k, int b_block);
+
+qg_status qgemm_f8(const uint8_t *A, const float *A_scales, const uint8_t *B, const float *B_scales,
+                   const void *bias, void *C, int m, int n, int k, int b_block, qg_dtype out_dtype,
+                   qg_dtype bias_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+qg_status qgemm_f8_grouped(const uint8_t *A, const float *A_scales, const int32_t *offsets,
+                           const uint8_t *B, const float *B_scales, const void *bias, void *C,
+                           int rows, int n, int k, int experts, qg_dtype out_dtype,
+                           qg_dtype bias_dtype, void *stream);
+
+/* Gated block on F8 operands: both projections, the activation and the product in
+ * one kernel.  With g = value(A) . value(B[0 .. inter))^T and u that of
+ * B[inter .. 2 inter):
+ *     H[m, i] = RNE_out(act(g) * u),   act(g) = g * sigmoid(y),
+ *     QG_GATE_SILU: y = g;   QG_GATE_GELU (its tanh form): y = 2 sqrt(2 / pi)
+ *     (g + 0.044715 g^3)
+ *   A        device codes [m, k], A_scales by rows [blocks(k), m]
+ *   B        device codes [2 inter, k], the gate's channels before the up
+ *            projection's, B_scales by blocks [2 inter / 128, blocks(k)]
+ *   H        device [m, inter] in out_dtype (QG_BF16, QG_FP16 or QG_FP32)
+ *   GU       device [m, 2 inter] in out_dtype, [g | u] for the backward pass, or
+ *            NULL.  H comes from the unrounded sums either way.
+ *   Tile multiples: inter % 128 == 0, k % 16 == 0; m any value >= 0.
+ *   Limits, alignment and scales as for qgemm_f8 with n = 2 inter; GU 16 bytes.
+ *
+ * qgated_f8_backward: the gradients of the block's operands from dH, the gradient
+ * of H, and the GU that the forward call saved:
+ *     dg = dH * u * act'(g),  du = dH * act(g)   in fp32;  D = [dg | du]
+ *     dX = RNE(value(D) . value(W)),  dW = RNE(value(D^T) . value(X^T)^T)
+ *   D is quantized by rows for dX and its transpose by rows for dW, both as by
+ *   qquantize_f8 (which makes XT and WT): the one rounding besides the results'.
+ *   dH       device [m, inter], GU device [m, 2 inter], in dtype (QG_BF16 or QG_FP16)
+ *   XT       device codes [k, R] of the transposed input, R = m rounded up to 16
+ *            (values past m zeros), XT_scales by rows [blocks(m), k]; unused
+ *            (NULL) without dW
+ *   WT       device codes [k, 2 inter] of the transposed weight, WT_scales by blocks
+ *            [blocks(k), 2 inter / 128]; unused (NULL) without dX
+ *   dX       device [m, k] in dx_dtype, or NULL;  dW device [2 inter, k] in
+ *            dw_dtype, or NULL (both dtypes QG_BF16, QG_FP16 or QG_FP32; that of
+ *            a NULL is not looked at)
+ *   m == 0: dW, if wanted, is filled with zeros.
+ *   Tile multiples: inter % 128 == 0, k % 16 == 0; inter at most 2^30 - 128.
+ *   Alignment: matrices 16 bytes, scales 4.
+ *   workspace: required, 256-byte aligned, at least
+ *   qgated_f8_backward_workspace_size(m, inter, k) bytes (0 for sizes the call
+ *   refuses and for m == 0).  Calls that share one must not overlap. */
+enum { QG_GATE_SILU = 0, QG_GATE_GELU = 1 };
+
+qg_status qgated_f8(const uint8_t *A, const float *A_scales, const uint8_t *B, const float *B_scales,
+                    void *H, void *GU, int m, int inter, int k, int act, qg_dtype out_dtype,
+                    void *stream);
+
+size_t qgated_f8_backward_workspace_size(int m, int inter, int k);
+
+qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT,
+                             const float *XT_scales, const uint8_t *WT, const float *WT_scales,
+                             void *dX, void *dW, int m, int inter, int k, int act, qg_dtype dtype,
+                             qg_dtype dx_dtype, qg_dtype dw_dtype, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Top-k MoE with SiLU-gated int4 experts  (acext User Guide (v1.7), 1.2.3

@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from ._abi import (QG_BF16, QG_FP16, QG_FP32, QG_LAYOUT_PORTABLE, QG_LAYOUT_TILED,
+from ._abi import (QG_BF16, QG_FP16, QG_FP32, QG_GATE_GELU, QG_GATE_SILU, QG_LAYOUT_PORTABLE, QG_LAYOUT_TILED,
                    QG_MOE_NORM_NONE, QG_MOE_RENORMALIZE, QG_NONE, QG_W8A8_PER_CHANNEL,
                    QG_W8A8_PER_TOKEN, QGemmError, check, lib)
 
@@ -24,6 +24,8 @@ __all__ = [
     "w8a8_workspace_size", "embed_w4", "embed_w8", "read_probe", "lds_probe", "set_override", "clear_override",
     "moe_grouped_noalloc", "quantize_mx4", "dequant_mx4", "repack_mx4", "unrepack_mx4",
     "gemm_mx4a16", "gemm_mx4a4", "gemm_mx4a16_grouped", "mx4_workspace_size",
+    "quantize_f8", "dequant_f8", "gemm_f8", "gemm_f8_grouped", "gated_f8", "gated_f8_backward",
+    "f8_workspace_size", "gated_f8_backward_workspace_size",
 ]
 
 _CODES = {torch.bfloat16: QG_BF16, torch.float16: QG_FP16, torch.float32: QG_FP32}
@@ -745,6 +747,283 @@ def gemm_mx4a16_grouped(A: torch.Tensor, offsets: torch.Tensor, B_tiled: torch.T
               rows, n, k, E, _CODES[A.dtype], QG_NONE if bias is None else _CODES[bias.dtype],
               _mx4_stream(dev))
     return C if out is None else C.reshape(rows, n)
+
+
+# -- block-scaled 8-bit floats (F8) ----------------------------------------------
+
+_F8 = torch.float8_e4m3fn
+_F32 = torch.float32
+_GATES = {"silu": QG_GATE_SILU, "gelu": QG_GATE_GELU}
+
+
+def _f8_blocks(x: int) -> int:
+    return -(-x // 128)
+
+
+def _f8_scale_shape(rows: int, k: int, block: int) -> tuple:
+    return (_f8_blocks(k), rows) if block == 1 else (_f8_blocks(rows), _f8_blocks(k))
+
+
+def _f8_size(func: str, *sizes: int) -> None:
+    if max(sizes) > _MX4_MOST:
+        raise QGemmError(func, 7, f"sizes must be below 2^31 (got {max(sizes)})")
+
+
+def _f8_block(func: str, block: int) -> None:
+    if block != 1 and block != 128:
+        raise QGemmError(func, 9, f"block must be 1 or 128 (got {block})")
+
+
+def _check_f8_pair(func: str, codes: torch.Tensor, scales: torch.Tensor, block: int,
+                   names=("codes", "scales"), lead: tuple = ()) -> tuple:
+    """(rows, k) of a codes / scales pair (after the leading dimensions)."""
+    cs, at = codes.shape, len(lead)
+    if codes.dtype == _F8 and scales.dtype == _F32 and len(cs) == at + 2 and (at == 0 or cs[:at] == lead):
+        rows, k = cs[at], cs[at + 1]
+        _f8_size(func, rows, k)
+        want = (*lead, *_f8_scale_shape(rows, k, block))
+        if k % 16 == 0 and scales.shape == want:
+            return rows, k
+        _mx4_multiple(func, k, 16)
+        _need(False, func, _SHAPE, f"{names[1]} must be {list(want)} (got {list(scales.shape)})")
+    _need(codes.dtype == _F8 and scales.dtype == _F32, func, _DTYPE,
+          f"{names[0]} must be float8_e4m3fn and {names[1]} float32")
+    _need(False, func, _SHAPE, f"{names[0]} must be {list(lead)} + [rows, k] (got {list(cs)})")
+
+
+def _f8_out_dtype(func: str, out: Optional[torch.Tensor], dtype: torch.dtype, m: int, n: int) -> torch.dtype:
+    if out is not None:
+        dtype = out.dtype
+        _check_out(func, out, dtype, m, n)
+    if dtype not in _CODES:
+        raise QGemmError(func, _DTYPE, f"the result must be bf16, fp16 or fp32 (got {dtype})")
+    return dtype
+
+
+def quantize_f8(X: torch.Tensor, block: int = 1, transposed: bool = False) -> tuple:
+    """F8 quantization (e4m3 codes, power-of-two scales) of X (bf16, fp16 or fp32).
+
+    block=1: X [..., k], leading dimensions flattened to rows; one scale per
+    row and 128 of k: (codes [rows, k], scales [ceil(k/128), rows]).
+    block=128: X [rows, k], or [E, rows, k] for a stack of matrices; one scale
+    per 128 x 128: (codes like X, scales [(E,) ceil(rows/128), ceil(k/128)]).
+    transposed: also, in the same pass, the codes [(E,) k, R] of each matrix's
+    transpose, R = rows rounded up to 16 (zeros), and their scales: by rows
+    (block=1) [ceil(rows/128), k], by blocks those of the matrix, transposed.
+    """
+    f = "qquantize_f8"
+    if X.dtype not in _CODES or X.dim() < 1:
+        raise QGemmError(f, _DTYPE, f"X must be bf16, fp16 or fp32 (got {X.dtype})")
+    _f8_block(f, block)
+    k = X.shape[-1]
+    _mx4_multiple(f, k, 16)
+    if block == 1:
+        lead, rows = (), X.shape[:-1].numel()
+    else:
+        _need(X.dim() in (2, 3), f, _SHAPE, f"X must be [rows, k] or [E, rows, k] (got {list(X.shape)})")
+        lead, rows = tuple(X.shape[:-2]), X.shape[-2]
+    stack = lead[0] if lead else 1
+    _f8_size(f, rows, k, stack)
+    dev = _mx4_devices(f, (X,), ("X",))
+    Q = X.new_empty((*lead, rows, k), dtype=_F8)
+    S = X.new_empty((*lead, *_f8_scale_shape(rows, k, block)), dtype=_F32)
+    out = (Q, S)
+    if transposed:
+        out += (X.new_empty((*lead, k, (rows + 15) // 16 * 16), dtype=_F8),
+                X.new_empty((*lead, *_f8_scale_shape(k, rows, block)), dtype=_F32))
+    if stack:
+        ptrs = [t.data_ptr() for t in out] + [None] * (4 - len(out))
+        _mx4_call(f, dev, X.data_ptr(), stack, rows, k, _CODES[X.dtype], block, *ptrs, _mx4_stream(dev))
+    return out
+
+
+def dequant_f8(codes: torch.Tensor, scales: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+               block: int = 1) -> torch.Tensor:
+    """F8 codes [rows, k] (block=128: or [E, rows, k]) and scales -> values in out_dtype."""
+    f = "qdequant_f8"
+    if out_dtype not in _CODES:
+        raise QGemmError(f, _DTYPE, f"out_dtype must be bf16, fp16 or fp32 (got {out_dtype})")
+    _f8_block(f, block)
+    lead = tuple(codes.shape[:1]) if block == 128 and codes.dim() == 3 else ()
+    rows, k = _check_f8_pair(f, codes, scales, block, lead=lead)
+    _f8_size(f, *lead, 0)
+    dev = _mx4_devices(f, (codes, scales), ("codes", "scales"))
+    out = codes.new_empty(codes.shape, dtype=out_dtype)
+    if out.numel():
+        _mx4_call(f, dev, codes.data_ptr(), scales.data_ptr(), out.data_ptr(), lead[0] if lead else 1, rows, k,
+                  block, _CODES[out_dtype], _mx4_stream(dev))
+    return out
+
+
+def f8_workspace_size(m: int, n: int, k: int, b_block: int = 128) -> int:
+    if min(m, n, k) < 0 or max(m, n, k) > _MX4_MOST:
+        return 0   # no problem the library takes
+    return int(lib().qgemm_f8_workspace_size(m, n, k, b_block))
+
+
+def _f8_workspace(need: int, like: torch.Tensor, given: Optional[torch.Tensor]):
+    """(tensor, address, bytes) of workspace: the caller's, else a fresh one
+    when the library asks for any."""
+    if given is not None:
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if need == 0:
+        return None, None, 0
+    ws = like.new_empty((need,), dtype=_U8)
+    return ws, ws.data_ptr(), need
+
+
+def gemm_f8(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_scales: torch.Tensor,
+            bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+            b_block: int = 128, out: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C [m, n] = value(A) . value(B)^T (+ bias): codes A [m, k] and B [n, k]
+    (float8_e4m3fn), A_scales by rows [ceil(k/128), m], B_scales by blocks
+    [ceil(n/128), ceil(k/128)] or, b_block=1, by rows [ceil(k/128), n].  The
+    scales are any fp32 numbers."""
+    f = "qgemm_f8"
+    _f8_block(f, b_block)
+    m, k = _check_f8_pair(f, A, A_scales, 1, ("A", "A_scales"))
+    n, kb = _check_f8_pair(f, B, B_scales, b_block, ("B", "B_scales"))
+    if k != kb:
+        raise QGemmError(f, _SHAPE, f"A and B must have the same k (got {k} and {kb})")
+    if bias is not None:
+        _check_bias(f, bias, n)
+    out_dtype = _f8_out_dtype(f, out, out_dtype, m, n)
+    dev = _mx4_devices(f, (A, A_scales, B, B_scales, bias, out, workspace),
+                       ("A", "A_scales", "B", "B_scales", "bias", "out", "workspace"))
+    C = out if out is not None else A.new_empty((m, n), dtype=out_dtype)
+    need = lib().qgemm_f8_workspace_size(m, n, k, b_block) if workspace is None else 0
+    ws, ws_ptr, ws_bytes = _f8_workspace(need, A, workspace)
+    _mx4_call(f, dev, A.data_ptr(), A_scales.data_ptr(), B.data_ptr(), B_scales.data_ptr(), _ptr(bias),
+              C.data_ptr(), m, n, k, b_block, _CODES[out_dtype], QG_NONE if bias is None else _CODES[bias.dtype],
+              ws_ptr, ws_bytes, _mx4_stream(dev))
+    return C if out is None else C.reshape(m, n)
+
+
+def gemm_f8_grouped(A: torch.Tensor, A_scales: torch.Tensor, offsets: torch.Tensor, B: torch.Tensor,
+                    B_scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    out_dtype: torch.dtype = torch.bfloat16,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of A
+    [rows, k] times expert e's weight.
+
+    offsets int32 [E + 1], non-decreasing, on the device; B [E, n, k] and
+    B_scales [E, ceil(n/128), ceil(k/128)] (quantize_f8 with block=128 of the
+    stacked experts); bias [E, n].  Returns [rows, n]; rows of no expert are left as
+    they were in `out` (undefined without one).
+    """
+    f = "qgemm_f8_grouped"
+    rows, k = _check_f8_pair(f, A, A_scales, 1, ("A", "A_scales"))
+    if offsets.dtype != torch.int32:
+        raise QGemmError(f, _DTYPE, f"offsets must be int32 (got {offsets.dtype})")
+    _need(offsets.dim() == 1 and offsets.numel() >= 2, f, _SHAPE, "offsets must be [E + 1], E >= 1")
+    E = offsets.numel() - 1
+    n, kb = _check_f8_pair(f, B, B_scales, 128, ("B", "B_scales"), lead=(E,))
+    if k != kb:
+        raise QGemmError(f, _SHAPE, f"A and B must have the same k (got {k} and {kb})")
+    if E > 65536:
+        raise QGemmError(f, 7, f"at most 65536 experts (got {E})")
+    if bias is not None and not (bias.dtype in _ACT and bias.shape == (E, n)):
+        _need(bias.dtype in _ACT, f, _DTYPE, f"bias must be bf16 or fp16 (got {bias.dtype})")
+        _need(_shape(bias) == (E, n), f, _SHAPE, f"bias must be [{E}, {n}] (got {list(bias.shape)})")
+    out_dtype = _f8_out_dtype(f, out, out_dtype, rows, n)
+    dev = _mx4_devices(f, (A, A_scales, offsets, B, B_scales, bias, out),
+                       ("A", "A_scales", "offsets", "B", "B_scales", "bias", "out"))
+    C = out if out is not None else A.new_empty((rows, n), dtype=out_dtype)
+    _mx4_call(f, dev, A.data_ptr(), A_scales.data_ptr(), offsets.data_ptr(), B.data_ptr(), B_scales.data_ptr(),
+              _ptr(bias), C.data_ptr(), rows, n, k, E, _CODES[out_dtype],
+              QG_NONE if bias is None else _CODES[bias.dtype], _mx4_stream(dev))
+    return C if out is None else C.reshape(rows, n)
+
+
+def _gate(func: str, act: str) -> int:
+    if act not in _GATES:
+        raise QGemmError(func, 9, f"act must be one of {sorted(_GATES)} (got {act!r})")
+    return _GATES[act]
+
+
+def gated_f8(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_scales: torch.Tensor,
+             act: str = "silu", out_dtype: torch.dtype = torch.bfloat16, return_gu: bool = False,
+             out: Optional[torch.Tensor] = None):
+    """Gated block: H [m, inter] = act(g) * u with g = value(A) . value(B[:inter])^T
+    and u that of B[inter:]; act "silu" or "gelu" (its tanh form).  A [m, k] with
+    scales by rows, B [2 inter, k] with scales by blocks, inter % 128 == 0.
+    return_gu: (H, GU), GU [m, 2 inter] = [g | u], which the backward pass takes."""
+    f = "qgated_f8"
+    code = _gate(f, act)
+    m, k = _check_f8_pair(f, A, A_scales, 1, ("A", "A_scales"))
+    n, kb = _check_f8_pair(f, B, B_scales, 128, ("B", "B_scales"))
+    if k != kb:
+        raise QGemmError(f, _SHAPE, f"A and B must have the same k (got {k} and {kb})")
+    if n % 256:
+        raise QGemmError(f, 7, f"B must hold 2 inter rows, inter a multiple of 128 (got {n})")
+    inter = n // 2
+    out_dtype = _f8_out_dtype(f, out, out_dtype, m, inter)
+    dev = _mx4_devices(f, (A, A_scales, B, B_scales, out), ("A", "A_scales", "B", "B_scales", "out"))
+    H = out if out is not None else A.new_empty((m, inter), dtype=out_dtype)
+    GU = A.new_empty((m, n), dtype=out_dtype) if return_gu else None
+    _mx4_call(f, dev, A.data_ptr(), A_scales.data_ptr(), B.data_ptr(), B_scales.data_ptr(), H.data_ptr(), _ptr(GU),
+              m, inter, k, code, _CODES[out_dtype], _mx4_stream(dev))
+    H = H if out is None else H.reshape(m, inter)
+    return (H, GU) if return_gu else H
+
+
+def gated_f8_backward_workspace_size(m: int, inter: int, k: int) -> int:
+    if min(m, inter, k) < 0 or max(m, inter, k) > _MX4_MOST:
+        return 0   # no problem the library takes
+    return int(lib().qgated_f8_backward_workspace_size(m, inter, k))
+
+
+def gated_f8_backward(dH: torch.Tensor, GU: torch.Tensor, XT: Optional[torch.Tensor],
+                      XT_scales: Optional[torch.Tensor], WT: Optional[torch.Tensor],
+                      WT_scales: Optional[torch.Tensor], act: str = "silu",
+                      dx_dtype: torch.dtype = torch.bfloat16, dw_dtype: torch.dtype = torch.bfloat16,
+                      workspace: Optional[torch.Tensor] = None) -> tuple:
+    """Gradients (dX [m, k], dW [2 inter, k]) of gated_f8 from dH [m, inter] and
+    the GU [m, 2 inter] it returned (both bf16 or fp16).
+
+    XT [k, R], XT_scales: the input's transpose and WT [k, 2 inter], WT_scales
+    the weight's, as quantize_f8(X, transposed=True) and quantize_f8(W, block=128,
+    transposed=True) return them.  Without XT there is no dW, without WT no dX
+    (None).  Inside, the gradient of [g | u] is quantized to F8 by rows, for dW
+    along the tokens."""
+    f = "qgated_f8_backward"
+    code = _gate(f, act)
+    _need(dH.dtype in _ACT and GU.dtype == dH.dtype, f, _DTYPE, "dH and GU must both be bf16 or fp16")
+    _need(dH.dim() == 2 and _shape(GU) == (dH.shape[0], 2 * dH.shape[1]), f, _SHAPE,
+          f"dH must be [m, inter] and GU [m, 2 inter] (got {list(dH.shape)} and {list(GU.shape)})")
+    m, inter = dH.shape
+    if inter % 128:
+        raise QGemmError(f, 7, f"inter must be a multiple of 128 (got {inter})")
+    _need(XT is not None or WT is not None, f, 1, "XT (for dW) or WT (for dX) is needed")
+    k = None
+    if WT is not None:
+        _need(WT_scales is not None, f, 1, "WT_scales is needed with WT")
+        k, n = _check_f8_pair(f, WT, WT_scales, 128, ("WT", "WT_scales"))
+        _need(n == 2 * inter, f, _SHAPE, f"WT must be [k, {2 * inter}] (got {list(WT.shape)})")
+    if XT is not None:
+        _need(XT_scales is not None, f, 1, "XT_scales is needed with XT")
+        kx, r = _check_f8_pair(f, XT, XT_scales, 1, ("XT", "XT_scales"))
+        _need(r == (m + 15) // 16 * 16 and k in (None, kx), f, _SHAPE,
+              f"XT must be [k, {(m + 15) // 16 * 16}], WT [k, {2 * inter}] (got k = {kx}, {list(XT.shape)})")
+        k = kx
+    _mx4_multiple(f, k, 16)
+    _f8_size(f, m, 2 * inter, k)
+    for name, dtype, used in (("dx_dtype", dx_dtype, WT), ("dw_dtype", dw_dtype, XT)):
+        if used is not None and dtype not in _CODES:
+            raise QGemmError(f, _DTYPE, f"{name} must be bf16, fp16 or fp32 (got {dtype})")
+    dev = _mx4_devices(f, (dH, GU, XT, XT_scales, WT, WT_scales, workspace),
+                       ("dH", "GU", "XT", "XT_scales", "WT", "WT_scales", "workspace"))
+    dX = None if WT is None else dH.new_empty((m, k), dtype=dx_dtype)
+    dW = None if XT is None else dH.new_empty((2 * inter, k), dtype=dw_dtype)
+    if k == 0:
+        return dX, dW
+    need = lib().qgated_f8_backward_workspace_size(m, inter, k) if workspace is None else 0
+    ws, ws_ptr, ws_bytes = _f8_workspace(need, dH, workspace)
+    _mx4_call(f, dev, dH.data_ptr(), GU.data_ptr(), _ptr(XT), _ptr(XT_scales), _ptr(WT), _ptr(WT_scales), _ptr(dX),
+              _ptr(dW), m, inter, k, code, _CODES[dH.dtype], 0 if dX is None else _CODES[dx_dtype],
+              0 if dW is None else _CODES[dw_dtype], ws_ptr, ws_bytes, _mx4_stream(dev))
+    return dX, dW
 
 
 # -- measurement probe -----------------------------------------------------------

@@ -23,6 +23,7 @@ QG_NONE, QG_BF16, QG_FP16, QG_FP32 = 0, 1, 2, 3
 QG_W8A8_PER_TENSOR, QG_W8A8_PER_CHANNEL, QG_W8A8_PER_TOKEN = 0, 1, 2
 QG_LAYOUT_PORTABLE, QG_LAYOUT_TILED = 0, 1
 QG_MOE_NORM_NONE, QG_MOE_RENORMALIZE = 0, 1
+QG_GATE_SILU, QG_GATE_GELU = 0, 1
 
 _P = ctypes.c_void_p
 _INT = ctypes.c_int
@@ -61,6 +62,15 @@ SIGNATURES = {
     "qgemm_mx4a16": (_ST, [_P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P, _SZ, _P]),
     "qgemm_mx4a4": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P, _SZ, _P]),
     "qgemm_mx4a16_grouped": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT, _P]),
+    "qquantize_f8": (_ST, [_P, _INT, _INT, _INT, _INT, _INT, _P, _P, _P, _P, _P]),
+    "qdequant_f8": (_ST, [_P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P]),
+    "qgemm_f8_workspace_size": (_SZ, [_INT, _INT, _INT, _INT]),
+    "qgemm_f8": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT, _P, _SZ, _P]),
+    "qgemm_f8_grouped": (_ST, [_P, _P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT, _P]),
+    "qgated_f8": (_ST, [_P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _P]),
+    "qgated_f8_backward_workspace_size": (_SZ, [_INT, _INT, _INT]),
+    "qgated_f8_backward": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT, _INT,
+                                 _P, _SZ, _P]),
     "qmoe_workspace_size": (_SZ, [_INT, _INT, _INT, _INT, _INT]),
     "qmoe_grouped": (_ST, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _INT, _INT, _INT, _INT, _INT, _INT,
                            _INT, _P, _P, _P, _SZ, _P]),

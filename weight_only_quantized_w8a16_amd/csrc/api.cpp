@@ -439,6 +439,217 @@ qg_status qgemm_mx4a16_grouped(const void *A, const int32_t *offsets, const uint
 }
 
 // ---------------------------------------------------------------------------
+// Block-scaled 8-bit floats (F8)
+// ---------------------------------------------------------------------------
+static constexpr int kF8Most = INT32_MAX - 255;
+static bool f8_out_ok(qg_dtype d) { return act_ok(d) || d == QG_FP32; }
+static size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+qg_status qquantize_f8(const void *X, int stack, int rows, int k, qg_dtype x_dt, int block,
+                       uint8_t *Q, float *S, uint8_t *QT, float *ST, void *stream) {
+  if (stack < 1 || rows < 0 || k < 0 || (block == 1 && stack != 1)) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;   // nothing to convert; pointers unused
+  if (!X || !Q != !S || !QT != !ST || (!Q && !QT)) return QG_ERR_NULL;
+  if (!f8_out_ok(x_dt)) return QG_ERR_DTYPE;
+  if (block != 1 && block != 128) return QG_ERR_MODE;
+  if (k % 16 != 0 || rows > kF8Most || k > kF8Most) return QG_ERR_UNSUPPORTED;
+  if (!aligned(X, 16) || !aligned(Q, 16) || !aligned(QT, 16) || !aligned(S, 4) || !aligned(ST, 4))
+    return QG_ERR_ALIGN;
+  const qg::F8Quantize q{X, stack, rows, k, static_cast<int>(x_dt), block, Q, S, QT, ST};
+  return mx4_status(qg::launch_quantize_f8(q, as_stream(stream)));
+}
+
+qg_status qdequant_f8(const uint8_t *Q, const float *S, void *out, int stack, int rows, int k,
+                      int block, qg_dtype out_dt, void *stream) {
+  if (stack < 1 || rows < 0 || k < 0 || (block == 1 && stack != 1)) return QG_ERR_SHAPE;
+  if (rows == 0 || k == 0) return QG_OK;   // nothing to convert; pointers unused
+  if (!Q || !S || !out) return QG_ERR_NULL;
+  if (!f8_out_ok(out_dt)) return QG_ERR_DTYPE;
+  if (block != 1 && block != 128) return QG_ERR_MODE;
+  if (k % 16 != 0 || rows > kF8Most || k > kF8Most) return QG_ERR_UNSUPPORTED;
+  if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(S, 4)) return QG_ERR_ALIGN;
+  return mx4_status(qg::launch_dequant_f8(Q, S, out, stack, rows, k, block, static_cast<int>(out_dt),
+                                          as_stream(stream)));
+}
+
+size_t qgemm_f8_workspace_size(int m, int n, int k, int b_block) {
+  if (m <= 0 || n <= 0 || k <= 0 || n % 16 != 0 || k % 16 != 0 || m > kF8Most || n > kF8Most ||
+      k > kF8Most || (b_block != 1 && b_block != 128))
+    return 0;
+  return up256(qg::f8_workspace_bytes(m, n, k, b_block));
+}
+
+// experts < 0: dense.
+static qg_status f8_gemm(const uint8_t *A, const float *AS, const int32_t *offsets, const uint8_t *B,
+                         const float *BS, const void *bias, void *C, int m, int n, int k, int experts,
+                         int b_block, qg_dtype out, qg_dtype bias_dt, void *workspace,
+                         size_t ws_bytes, void *stream) {
+  const bool grouped = experts >= 0;
+  if (m < 0 || n < 0 || k <= 0 || (grouped && experts == 0)) return QG_ERR_SHAPE;
+  if (m == 0 || n == 0) return QG_OK;   // nothing to compute; pointers unused
+  if (!A || !AS || !B || !BS || !C || (grouped && !offsets)) return QG_ERR_NULL;
+  if (bias_dt != QG_NONE && !bias) return QG_ERR_NULL;
+  if (!f8_out_ok(out)) return QG_ERR_DTYPE;
+  if (bias_dt == QG_NONE ? bias != nullptr : !act_ok(bias_dt)) return QG_ERR_DTYPE;
+  if (b_block != 1 && b_block != 128) return QG_ERR_MODE;
+  if (n % 16 != 0 || k % 16 != 0 || m > kF8Most || n > kF8Most || k > kF8Most ||
+      (grouped && experts > 65536))
+    return QG_ERR_UNSUPPORTED;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(AS, 4) || !aligned(BS, 4) ||
+      !aligned(offsets, 4) || !aligned(bias, 2))
+    return QG_ERR_ALIGN;
+  if (workspace && ws_bytes && !aligned(workspace, 256)) return QG_ERR_ALIGN;
+  qg::F8Args a{};
+  a.A = A;
+  a.SA = AS;
+  a.B = B;
+  a.SB = BS;
+  a.b_block = b_block;
+  a.bias = static_cast<const uint16_t *>(bias);
+  a.C = C;
+  a.M = m;
+  a.N = n;
+  a.K = k;
+  a.out = static_cast<int>(out);
+  a.bias_dt = static_cast<int>(bias_dt);
+  a.offsets = offsets;
+  a.E = grouped ? experts : 0;
+  a.ws = workspace;
+  a.ws_bytes = workspace ? ws_bytes : 0;
+  return mx4_status(qg::launch_f8_gemm(a, as_stream(stream)));
+}
+
+qg_status qgemm_f8(const uint8_t *A, const float *AS, const uint8_t *B, const float *BS,
+                   const void *bias, void *C, int m, int n, int k, int b_block, qg_dtype out,
+                   qg_dtype bias_dt, void *workspace, size_t ws_bytes, void *stream) {
+  return f8_gemm(A, AS, nullptr, B, BS, bias, C, m, n, k, -1, b_block, out, bias_dt, workspace,
+                 ws_bytes, stream);
+}
+
+qg_status qgemm_f8_grouped(const uint8_t *A, const float *AS, const int32_t *offsets,
+                           const uint8_t *B, const float *BS, const void *bias, void *C, int rows,
+                           int n, int k, int experts, qg_dtype out, qg_dtype bias_dt, void *stream) {
+  if (experts < 0) return QG_ERR_SHAPE;
+  return f8_gemm(A, AS, offsets, B, BS, bias, C, rows, n, k, experts, 128, out, bias_dt, nullptr, 0,
+                 stream);
+}
+
+static bool gate_ok(int act) { return act == QG_GATE_SILU || act == QG_GATE_GELU; }
+static bool gated_sizes_ok(int m, int inter, int k) {
+  return inter % 128 == 0 && k % 16 == 0 && m <= kF8Most && inter <= (1 << 30) - 128 && k <= kF8Most;
+}
+
+qg_status qgated_f8(const uint8_t *A, const float *AS, const uint8_t *B, const float *BS, void *H,
+                    void *GU, int m, int inter, int k, int act, qg_dtype out, void *stream) {
+  if (m < 0 || inter < 0 || k <= 0) return QG_ERR_SHAPE;
+  if (m == 0 || inter == 0) return QG_OK;   // nothing to compute; pointers unused
+  if (!A || !AS || !B || !BS || !H) return QG_ERR_NULL;
+  if (!f8_out_ok(out)) return QG_ERR_DTYPE;
+  if (!gate_ok(act)) return QG_ERR_MODE;
+  if (!gated_sizes_ok(m, inter, k)) return QG_ERR_UNSUPPORTED;
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(H, 16) || !aligned(GU, 16) || !aligned(AS, 4) ||
+      !aligned(BS, 4))
+    return QG_ERR_ALIGN;
+  qg::F8Args a{};
+  a.A = A;
+  a.SA = AS;
+  a.B = B;
+  a.SB = BS;
+  a.b_block = 128;
+  a.C = H;
+  a.M = m;
+  a.N = 2 * inter;
+  a.K = k;
+  a.out = static_cast<int>(out);
+  a.gated = true;
+  a.act = act;
+  a.GU = GU;
+  return mx4_status(qg::launch_f8_gemm(a, as_stream(stream)));
+}
+
+// The backward pass's workspace: D, D^T, their scales, and the products' K
+// slices (one product after the other).
+namespace {
+struct GatedWs {
+  size_t d, dt, sd, sdt, part, part_bytes, bytes;
+  GatedWs(int m, int inter, int k) {
+    const size_t n = 2 * static_cast<size_t>(inter), r = (static_cast<size_t>(m) + 15) / 16 * 16;
+    d = 0;
+    dt = d + up256(static_cast<size_t>(m) * n);
+    sd = dt + up256(n * r);
+    sdt = sd + up256(n / 128 * m * sizeof(float));
+    part = sdt + up256((static_cast<size_t>(m) + 127) / 128 * n * sizeof(float));
+    const size_t x = qg::f8_workspace_bytes(m, k, 2 * inter, 128),
+                 w = qg::f8_workspace_bytes(2 * inter, k, static_cast<int>(r), 1);
+    part_bytes = up256(x > w ? x : w);
+    bytes = part + part_bytes;
+  }
+};
+}  // namespace
+
+size_t qgated_f8_backward_workspace_size(int m, int inter, int k) {
+  if (m <= 0 || inter <= 0 || k <= 0 || !gated_sizes_ok(m, inter, k)) return 0;
+  return GatedWs(m, inter, k).bytes;
+}
+
+qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT, const float *XTS,
+                             const uint8_t *WT, const float *WTS, void *dX, void *dW, int m,
+                             int inter, int k, int act, qg_dtype dt, qg_dtype dx_dt, qg_dtype dw_dt,
+                             void *workspace, size_t ws_bytes, void *stream) {
+  if (m < 0 || inter < 0 || k <= 0) return QG_ERR_SHAPE;
+  if (inter == 0 || (m == 0 && !dW) || (!dX && !dW)) return QG_OK;   // nothing to compute
+  const bool some = m > 0;
+  if (some && (!dH || !GU || (dX && (!WT || !WTS)) || (dW && (!XT || !XTS)))) return QG_ERR_NULL;
+  if (!act_ok(dt) || (dX && !f8_out_ok(dx_dt)) || (dW && !f8_out_ok(dw_dt))) return QG_ERR_DTYPE;
+  if (!gate_ok(act)) return QG_ERR_MODE;
+  if (!gated_sizes_ok(m, inter, k)) return QG_ERR_UNSUPPORTED;
+  if (!aligned(dH, 16) || !aligned(GU, 16) || !aligned(XT, 16) || !aligned(WT, 16) ||
+      !aligned(dX, 16) || !aligned(dW, 16) || !aligned(XTS, 4) || !aligned(WTS, 4))
+    return QG_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (!some)
+    return mx4_status(qg::launch_fill_zero(dW, static_cast<size_t>(2 * inter) * k * (dw_dt == QG_FP32 ? 4 : 2), s));
+  const GatedWs ws(m, inter, k);
+  if (!workspace || ws_bytes < ws.bytes) return QG_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return QG_ERR_ALIGN;
+  uint8_t *w = static_cast<uint8_t *>(workspace);
+  uint8_t *D = dX ? w + ws.d : nullptr, *DT = dW ? w + ws.dt : nullptr;
+  float *SD = reinterpret_cast<float *>(w + ws.sd), *SDT = reinterpret_cast<float *>(w + ws.sdt);
+  const qg::F8GatedGrad g{dH, GU, m, inter, static_cast<int>(dt), act, D, SD, DT, SDT};
+  hipError_t e = qg::launch_gated_f8_grad(g, s);
+  if (e != hipSuccess) return mx4_status(e);
+  qg::F8Args a{};
+  a.N = k;
+  a.ws = w + ws.part;
+  a.ws_bytes = ws.part_bytes;
+  if (dX) {
+    a.A = D;
+    a.SA = SD;
+    a.B = WT;
+    a.SB = WTS;
+    a.b_block = 128;
+    a.C = dX;
+    a.M = m;
+    a.K = 2 * inter;
+    a.out = static_cast<int>(dx_dt);
+    if ((e = qg::launch_f8_gemm(a, s)) != hipSuccess) return mx4_status(e);
+  }
+  if (dW) {
+    a.A = DT;
+    a.SA = SDT;
+    a.B = XT;
+    a.SB = XTS;
+    a.b_block = 1;
+    a.C = dW;
+    a.M = 2 * inter;
+    a.K = (m + 15) / 16 * 16;
+    a.out = static_cast<int>(dw_dt);
+    if ((e = qg::launch_f8_gemm(a, s)) != hipSuccess) return mx4_status(e);
+  }
+  return QG_OK;
+}
+
+// ---------------------------------------------------------------------------
 // MoE
 // ---------------------------------------------------------------------------
 size_t qmoe_workspace_size(int tokens, int hidden, int inter, int experts, int topk) {

@@ -1,0 +1,338 @@
+// f8.hip -- conversions of the block-scaled 8-bit float format (F8): quantize
+// (by rows or by 128 x 128 blocks, transposed as well), read back, and the
+// gradient of the gated block's activation and product, quantized both ways
+// as the two products of the backward pass read it.  All of them are bound by
+// HBM (the smallest by a launch): a value is read once and its codes are
+// written once each.
+#include <algorithm>
+
+#include "f8_common.hpp"
+
+namespace qg {
+
+namespace {
+
+// Eight consecutive values of a row as fp32.
+template <int DT>
+__device__ __forceinline__ void load8(const void *X, size_t i, float (&v)[8]) {
+  if constexpr (DT == QG_FP32) {
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(X) + i);
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(X) + i + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(X) + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = bits_to_f32<DT>(static_cast<uint16_t>(a[e] & 0xFFFFu));
+      v[2 * e + 1] = bits_to_f32<DT>(static_cast<uint16_t>(a[e] >> 16));
+    }
+  }
+}
+
+// The maximum over the 16 lanes of a DPP row, in all of them (all active).
+__device__ __forceinline__ int max16(int x) {
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false));    // quad_perm 1 0 3 2
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false));    // quad_perm 2 3 0 1
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  return max(x, __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false)); // row_mirror
+}
+
+// Rows alone, one scale per 128 of k: 16 lanes a block, eight values each.
+template <int DT>
+__global__ __launch_bounds__(256) void k_f8_rows(const void *X, uint8_t *Q, float *S, uint32_t rows, uint32_t k) {
+  const uint32_t kb = f8_blocks(static_cast<int>(k)), groups = rows * kb, l = threadIdx.x & 15;
+  for (uint32_t g = blockIdx.x * 16 + (threadIdx.x >> 4); g < groups; g += gridDim.x * 16) {
+    const uint32_t row = g / kb, b = g - row * kb, col = b * 128 + 8 * l;
+    const size_t at = static_cast<size_t>(row) * k + col;
+    float v[8] = {};
+    if (col < k) load8<DT>(X, at, v);
+    int top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = f8_top(top, v[e]);
+    const F8Scale s(max16(top));
+    if (col < k) {
+      uint32_t lo = f8_pack4(v[0] * s.inv, v[1] * s.inv, v[2] * s.inv, v[3] * s.inv);
+      uint32_t hi = f8_pack4(v[4] * s.inv, v[5] * s.inv, v[6] * s.inv, v[7] * s.inv);
+      *reinterpret_cast<u32x2 *>(Q + at) = s.bad ? u32x2{0, 0} : u32x2{lo, hi};
+    }
+    if (l == 0) S[static_cast<size_t>(b) * rows + row] = s.scale;
+  }
+}
+
+// One 128 x 128 tile, 512 threads: thread t holds rows 4 (t / 16) .. + 3, columns
+// 8 (t % 16) .. + 7.  Writes the codes by rows and, through LDS, transposed, with
+// one scale per row (per column, transposed) of the tile, or one for all of it
+// (BLOCK).  Values past the matrix are zeros; the transposed rows are padded to a
+// multiple of 16 with the zeros' codes.  Called by all threads, again only
+// after a barrier.
+struct F8TileLds {
+  char codes[128 * 128];   // [column][row], 16-byte chunk c of column n at c ^ ((n / 8) % 8)
+  int top[128];
+};
+struct F8TileOut {
+  uint8_t *Q;       // [rows, ldq] or null
+  float *S;         // the tile's row scales (of this block of k), or its one scale
+  uint8_t *QT;      // [k, ldqt] or null
+  float *ST;        // the tile's column scales, or its one scale
+  size_t ldq, ldqt;
+};
+
+template <bool BLOCK, bool ROWS, bool COLS>
+__device__ __forceinline__ void f8_emit(const float (&v)[4][8], F8TileLds &L, const F8TileOut &o, int row0, int rows,
+                                        int col0, int k) {
+  const int t = threadIdx.x, r = 4 * (t >> 4), c = 8 * (t & 15);
+  int rtop[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rtop[p] = f8_top(rtop[p], v[p][e]);
+  if (BLOCK || COLS) {
+    if (t < 128) L.top[t] = 0;
+    __syncthreads();
+  }
+  if constexpr (BLOCK) {
+    const int m = max16(max(max(rtop[0], rtop[1]), max(rtop[2], rtop[3])));
+    if ((t & 15) == 0) atomicMax(&L.top[0], m);
+    __syncthreads();
+  } else if constexpr (COLS) {
+    // The wave's 16 rows of a column: lanes 16 and 32 apart, then LDS.
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int m = f8_top(f8_top(f8_top(f8_top(0, v[0][e]), v[1][e]), v[2][e]), v[3][e]);
+      m = max(m, __shfl_xor(m, 16));
+      m = max(m, __shfl_xor(m, 32));
+      if ((t & 63) < 16) atomicMax(&L.top[c + e], m);
+    }
+    __syncthreads();
+  }
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const F8Scale s(BLOCK ? L.top[0] : max16(rtop[p]));
+      const int row = row0 + r + p;
+      if (row < rows && col0 + c < k) {
+        const uint32_t lo = f8_pack4(v[p][0] * s.inv, v[p][1] * s.inv, v[p][2] * s.inv, v[p][3] * s.inv);
+        const uint32_t hi = f8_pack4(v[p][4] * s.inv, v[p][5] * s.inv, v[p][6] * s.inv, v[p][7] * s.inv);
+        *reinterpret_cast<u32x2 *>(o.Q + static_cast<size_t>(row) * o.ldq + col0 + c) =
+            s.bad ? u32x2{0, 0} : u32x2{lo, hi};
+      }
+      if (!BLOCK && (t & 15) == 0 && row < rows) o.S[r + p] = s.scale;
+    }
+    if (BLOCK && t == 0) o.S[0] = F8Scale(L.top[0]).scale;
+  }
+  if constexpr (COLS) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const F8Scale s(L.top[BLOCK ? 0 : c + e]);
+      const uint32_t w = f8_pack4(v[0][e] * s.inv, v[1][e] * s.inv, v[2][e] * s.inv, v[3][e] * s.inv);
+      *reinterpret_cast<uint32_t *>(L.codes + (c + e) * 128 + (((r >> 4) ^ (t & 7)) << 4) + (r & 15)) = s.bad ? 0 : w;
+    }
+    if (BLOCK ? t == 0 : t < 128 && col0 + t < k) o.ST[t] = F8Scale(L.top[t]).scale;
+    __syncthreads();
+    const int padded = f8_pad16(rows);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = 64 * i + (t >> 3), q = t & 7;
+      if (col0 + n < k && row0 + 16 * q < padded)
+        *reinterpret_cast<u32x4 *>(o.QT + static_cast<size_t>(col0 + n) * o.ldqt + row0 + 16 * q) =
+            *reinterpret_cast<const u32x4 *>(L.codes + n * 128 + ((q ^ ((n >> 3) & 7)) << 4));
+    }
+  }
+}
+
+// Matrix x, tile (rb, b) of a stack of [rows, k] matrices.
+template <int DT, bool BLOCK, bool ROWS, bool COLS>
+__global__ __launch_bounds__(512) void k_f8_tile(const void *X, uint8_t *Q, float *S, uint8_t *QT, float *ST, int rows,
+                                                 int k) {
+  __shared__ __attribute__((aligned(16))) F8TileLds L;
+  const uint32_t kb = f8_blocks(k), rb = f8_blocks(rows);
+  const uint32_t tiles = rb * kb, x = blockIdx.x / tiles, in = blockIdx.x - x * tiles, ri = in / kb, b = in - ri * kb;
+  const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
+  const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
+  const size_t base = static_cast<size_t>(x) * rows * k;
+  float v[4][8] = {};
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    if (row0 + r + p < rows && col0 + c < k) load8<DT>(X, base + static_cast<size_t>(row0 + r + p) * k + col0 + c, v[p]);
+  const size_t pad = f8_pad16(rows);
+  const F8TileOut o{
+      ROWS ? Q + base : nullptr,
+      ROWS ? S + (BLOCK ? static_cast<size_t>(x) * tiles + in : static_cast<size_t>(b) * rows + row0) : nullptr,
+      COLS ? QT + static_cast<size_t>(x) * k * pad : nullptr,
+      COLS ? ST + (BLOCK ? (static_cast<size_t>(x) * kb + b) * rb + ri : static_cast<size_t>(ri) * k + col0) : nullptr,
+      static_cast<size_t>(k), pad};
+  f8_emit<BLOCK, ROWS, COLS>(v, L, o, row0, rows, col0, k);
+}
+
+// D = [dh u act'(g) | dh act(g)] from GU = [g | u], tile (ri, b) of its two halves.
+template <int DT, bool ROWS, bool COLS>
+__global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const void *GU, uint8_t *D, float *SD,
+                                                       uint8_t *DT_, float *SDT, int rows, int inter, int act) {
+  __shared__ __attribute__((aligned(16))) F8TileLds L;
+  const uint32_t kb = static_cast<uint32_t>(inter) >> 7;
+  const uint32_t ri = blockIdx.x / kb, b = blockIdx.x - ri * kb;
+  const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
+  const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
+  const size_t wide = 2 * static_cast<size_t>(inter), pad = f8_pad16(rows);
+  float dg[4][8] = {}, du[4][8] = {};
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const size_t row = static_cast<size_t>(row0 + r + p);
+    if (row0 + r + p < rows) {
+      float h[8], g[8], u[8];
+      load8<DT>(dH, row * inter + col0 + c, h);
+      load8<DT>(GU, row * wide + col0 + c, g);
+      load8<DT>(GU, row * wide + inter + col0 + c, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float value;
+        const float slope = f8_gate_slope(g[e], act, value);
+        dg[p][e] = h[e] * u[e] * slope;
+        du[p][e] = h[e] * value;
+      }
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int n0 = col0 + half * inter;
+    const F8TileOut o{D, ROWS ? SD + static_cast<size_t>(n0 >> 7) * rows + row0 : nullptr, DT_,
+                      COLS ? SDT + static_cast<size_t>(ri) * wide + n0 : nullptr, wide, pad};
+    if (half) {
+      __syncthreads();
+      f8_emit<false, ROWS, COLS>(du, L, o, row0, rows, n0, 2 * inter);
+    } else {
+      f8_emit<false, ROWS, COLS>(dg, L, o, row0, rows, n0, 2 * inter);
+    }
+  }
+}
+
+// Codes and scales -> values: eight a thread.
+template <int DT, bool BLOCK>
+__global__ __launch_bounds__(256) void k_f8_dequant(const uint8_t *Q, const float *S, void *out, int stack, int rows,
+                                                    int k) {
+  const size_t vecs = static_cast<size_t>(stack) * rows * (static_cast<size_t>(k) >> 3), step = static_cast<size_t>(gridDim.x) * 256;
+  const uint32_t per = static_cast<uint32_t>(k) >> 3, kb = f8_blocks(k), rb = f8_blocks(rows);
+  for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < vecs; i += step) {
+    const size_t row = i / per;
+    const uint32_t b = static_cast<uint32_t>(i - row * per) >> 4;
+    size_t at;
+    if constexpr (BLOCK) {
+      const size_t x = row / static_cast<uint32_t>(rows);
+      at = (x * rb + ((row - x * rows) >> 7)) * kb + b;
+    } else {
+      at = static_cast<size_t>(b) * rows + row;
+    }
+    const float s = S[at];
+    const u32x2 w = *reinterpret_cast<const u32x2 *>(Q + i * 8);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const f32x2 lo = f8_unpack2<false>(w[e]), hi = f8_unpack2<true>(w[e]);
+      v[4 * e] = lo[0] * s;
+      v[4 * e + 1] = lo[1] * s;
+      v[4 * e + 2] = hi[0] * s;
+      v[4 * e + 3] = hi[1] * s;
+    }
+    if constexpr (DT == QG_FP32) {
+      float *p = static_cast<float *>(out) + i * 8;
+      *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(out) + i * 8) =
+          u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void k_fill_zero(u32x4 *p, size_t n) {
+  const size_t step = static_cast<size_t>(gridDim.x) * 256;
+  for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += step) p[i] = u32x4{0, 0, 0, 0};
+}
+
+constexpr uint64_t kLaunch = UINT32_MAX;   // threads of a launch
+
+template <int DT>
+hipError_t quantize_as(const F8Quantize &q, hipStream_t s) {
+  if (q.block == 1 && !q.QT) {
+    const uint64_t groups = static_cast<uint64_t>(q.rows) * f8_blocks(q.k);
+    if (groups > INT32_MAX) return hipErrorNotSupported;
+    const unsigned grid = static_cast<unsigned>(std::min<uint64_t>((groups + 15) / 16, 1u << 20));
+    hipLaunchKernelGGL(k_f8_rows<DT>, dim3(grid), dim3(256), 0, s, q.X, q.Q, q.S, static_cast<uint32_t>(q.rows),
+                       static_cast<uint32_t>(q.k));
+    return hipGetLastError();
+  }
+  const uint64_t tiles = static_cast<uint64_t>(f8_blocks(q.rows)) * f8_blocks(q.k);
+  if (tiles * q.stack * 512 > kLaunch) return hipErrorNotSupported;
+  const dim3 grid(static_cast<unsigned>(tiles * q.stack)), block(512);
+#define QG_F8_TILE(BLOCK, ROWS, COLS) \
+  hipLaunchKernelGGL((k_f8_tile<DT, BLOCK, ROWS, COLS>), grid, block, 0, s, q.X, q.Q, q.S, q.QT, q.ST, q.rows, q.k)
+  if (q.block == 1) {
+    if (q.Q) QG_F8_TILE(false, true, true);
+    else QG_F8_TILE(false, false, true);
+  } else if (!q.QT) {
+    QG_F8_TILE(true, true, false);
+  } else if (q.Q) {
+    QG_F8_TILE(true, true, true);
+  } else {
+    QG_F8_TILE(true, false, true);
+  }
+#undef QG_F8_TILE
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t dequant_as(const uint8_t *Q, const float *S, void *out, int stack, int rows, int k, int block, hipStream_t s) {
+  const uint64_t vecs = static_cast<uint64_t>(stack) * rows * (static_cast<uint64_t>(k) >> 3);
+  const dim3 grid(static_cast<unsigned>(std::min<uint64_t>((vecs + 255) / 256, 1u << 20)));
+  if (block == 1) hipLaunchKernelGGL((k_f8_dequant<DT, false>), grid, dim3(256), 0, s, Q, S, out, stack, rows, k);
+  else hipLaunchKernelGGL((k_f8_dequant<DT, true>), grid, dim3(256), 0, s, Q, S, out, stack, rows, k);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t grad_as(const F8GatedGrad &g, hipStream_t s) {
+  const uint64_t tiles = static_cast<uint64_t>(f8_blocks(g.m)) * (g.inter >> 7);
+  if (tiles * 512 > kLaunch) return hipErrorNotSupported;
+  const dim3 grid(static_cast<unsigned>(tiles)), block(512);
+#define QG_F8_GRAD(ROWS, COLS)                                                                                   \
+  hipLaunchKernelGGL((k_f8_gated_grad<DT, ROWS, COLS>), grid, block, 0, s, g.dH, g.GU, g.D, g.SD, g.DT, g.SDT, g.m, \
+                     g.inter, g.act)
+  if (g.D && g.DT) QG_F8_GRAD(true, true);
+  else if (g.D) QG_F8_GRAD(true, false);
+  else QG_F8_GRAD(false, true);
+#undef QG_F8_GRAD
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_f8(const F8Quantize &q, hipStream_t s) {
+  switch (q.dt) {
+    case QG_FP32: return quantize_as<QG_FP32>(q, s);
+    case QG_FP16: return quantize_as<QG_FP16>(q, s);
+    default: return quantize_as<QG_BF16>(q, s);
+  }
+}
+
+hipError_t launch_dequant_f8(const uint8_t *Q, const float *S, void *out, int stack, int rows, int k, int block,
+                             int out_dt, hipStream_t s) {
+  switch (out_dt) {
+    case QG_FP32: return dequant_as<QG_FP32>(Q, S, out, stack, rows, k, block, s);
+    case QG_FP16: return dequant_as<QG_FP16>(Q, S, out, stack, rows, k, block, s);
+    default: return dequant_as<QG_BF16>(Q, S, out, stack, rows, k, block, s);
+  }
+}
+
+hipError_t launch_fill_zero(void *p, size_t bytes, hipStream_t s) {
+  const size_t n = bytes / 16;
+  hipLaunchKernelGGL(k_fill_zero, dim3(static_cast<unsigned>(std::min<size_t>((n + 255) / 256, 4096))), dim3(256), 0, s,
+                     static_cast<u32x4 *>(p), n);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_f8_grad(const F8GatedGrad &g, hipStream_t s) {
+  return g.dt == QG_FP16 ? grad_as<QG_FP16>(g, s) : grad_as<QG_BF16>(g, s);
+}
+
+}  // namespace qg

@@ -1,0 +1,229 @@
+// f8_gemm.hip -- products of block-scaled 8-bit floats (F8):
+//   C[m, n] = sum_k value(A)[m, k] * value(B)[n, k] (+ bias[n]),
+// dense, grouped by expert, or gated (B's rows are gate and up channels, H =
+// act(g) * u) (include/qgemm.h).
+//
+// The scales are any fp32 numbers, so they cannot ride on the matrix
+// instruction (whose own are powers of two).  Scales change every 128 k, and
+// one 16 x 16 x 128 instruction covers just that: it multiplies on zero, and its
+// sum t is added as acc += t * (sa * sb) in fp32, four instructions of a lane
+// for every matrix instruction.  The instruction sums eight consecutive k at a
+// time and cuts each product at 2^-13 of the eight's largest (measured; all 8-bit
+// matrix instructions here do, and 16-bit ones run at half the rate), which on
+// normal operands is 3e-5 of a result; everything past the eights is fp32.  The
+// product sa * sb is rounded once, and C once.
+//
+// Weights are the row operand and activations the column operand, so lane
+// (nl, q) of a 16 x 16 accumulator holds row m = nl -- one activation scale --
+// and the four consecutive columns 4 q .. 4 q + 3.  Any order of k serves as long as
+// both operands use the same: lane (nl, q) takes the 16-byte chunks q and q + 4
+// of its row's 128 bytes.
+#include <algorithm>
+
+#include "f8_common.hpp"
+#include "row_groups.hpp"
+
+namespace qg {
+
+namespace {
+
+enum { kDense, kGrouped, kGated };   // forms
+
+struct F8Problem {
+  const uint8_t *A;
+  const float *SA;
+  const uint8_t *B;
+  const float *SB;
+  const uint16_t *bias;
+  void *C, *GU;
+  int M, N, K, bias_dt;   // N: channels of B, gate and up ones alike
+  const int32_t *offsets;
+  int E, act;
+};
+
+template <int OUT>
+__device__ __forceinline__ void store4(void *C, size_t off, f32x4 v) {
+  if constexpr (OUT == QG_FP32) {
+    *reinterpret_cast<f32x4 *>(static_cast<float *>(C) + off) = v;
+  } else {
+    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(C) + off) =
+        u32x2{pack2<OUT>(v[0], v[1]), pack2<OUT>(v[2], v[3])};
+  }
+}
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Streaming kernel, for few rows: a workgroup owns 16 rows and NT tiles of 16
+// columns (gated: NT / 2 gate tiles and the up tiles beside them), and its waves
+// take 128-k blocks in turn.  Nothing is shared between waves until their sums
+// meet in LDS.  Bound by HBM.
+// ---------------------------------------------------------------------------
+template <int NT, bool BROW>
+struct F8StreamBlock {
+  u32x4 w[NT][2], a[2];
+  float sa;
+  std::conditional_t<BROW, f32x4, float> sb[NT];
+};
+
+template <int OUT, int NT, int FORM, bool BROW>
+__global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
+  extern __shared__ __attribute__((aligned(16))) float red[];   // [wave][NT][64][4]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nwaves = blockDim.x >> 6;
+  const int nl = lane & 15, q = lane >> 4;
+  const int K = p.K, nb = f8_blocks(K), ntiles = p.N >> 4;
+  constexpr int OWN = FORM == kGated ? NT / 2 : NT;   // column tiles of C
+  const int half = ntiles >> 1, ctiles = FORM == kGated ? half : ntiles;
+  const int nt0 = blockIdx.x * OWN;
+  int row0 = (slab0 + static_cast<int>(blockIdx.y)) * 16, row1 = min(p.M, row0 + 16), e = 0;
+  if constexpr (FORM == kGrouped) {
+    RowGroups groups(p, 16);
+    if (!groups.find(slab0 + blockIdx.y, e, row0, row1)) return;
+  }
+  // Rows and column tiles past the end repeat the last; their sums are not stored.
+  const uint8_t *B = p.B + static_cast<size_t>(e) * p.N * K;
+  const float *SB = p.SB + static_cast<size_t>(e) * f8_blocks(p.N) * nb;
+  const uint8_t *wp[NT];
+  const float *sp[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int nt = min(nt0 + i % OWN, ctiles - 1) + (i >= OWN ? half : 0);
+    wp[i] = B + static_cast<size_t>(nt * 16 + nl) * K;
+    sp[i] = BROW ? SB + nt * 16 + 4 * q : SB + static_cast<size_t>(nt >> 3) * nb;
+  }
+  const int row = min(row0 + nl, row1 - 1);
+  const uint8_t *ap = p.A + static_cast<size_t>(row) * K;
+  const float *sap = p.SA + row;
+  using Block = F8StreamBlock<NT, BROW>;
+  auto load = [&](int kb, Block &f) {
+    // Chunks past K are read at the row's start and multiplied as zeros.
+    const size_t k0 = static_cast<size_t>(kb) * 128 + 16 * q, at0 = k0 < static_cast<size_t>(K) ? k0 : 0,
+                 at1 = k0 + 64 < static_cast<size_t>(K) ? k0 + 64 : 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f.w[i][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at0));
+      f.w[i][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at1));
+      if constexpr (BROW) f.sb[i] = *reinterpret_cast<const f32x4u *>(sp[i] + static_cast<size_t>(kb) * p.N);
+      else f.sb[i] = sp[i][kb];
+    }
+    f.a[0] = *reinterpret_cast<const u32x4 *>(ap + at0);
+    f.a[1] = *reinterpret_cast<const u32x4 *>(ap + at1);
+    f.sa = sap[static_cast<size_t>(kb) * p.M];
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto mma = [&](int kb, Block &f) {
+    if (kb * 128 + 128 > K) {   // a NaN code past K must not count: zeros on both sides
+      const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool past = kb * 128 + 64 * h + 16 * q >= K;
+        f.a[h] = past ? zero : f.a[h];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) f.w[i][h] = past ? zero : f.w[i][h];
+      }
+    }
+    const i32x8 a = f8_frag(f.a[0], f.a[1]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const f32x4 t = f8_mfma(f8_frag(f.w[i][0], f.w[i][1]), a);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (BROW) acc[i][v] += t[v] * (f.sa * f.sb[i][v]);
+        else acc[i][v] += t[v] * (f.sa * f.sb[i]);
+      }
+    }
+  };
+  for (int kb = wave; kb < nb; kb += nwaves) {
+    Block f;
+    load(kb, f);
+    mma(kb, f);
+  }
+  // The waves' sums meet in LDS and are added in wave order; a thread finishes
+  // four consecutive columns, the quads of a tile on neighbouring threads.
+#pragma unroll
+  for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4 *>(red + ((wave * NT + i) * 64 + lane) * 4) = acc[i];
+  __syncthreads();
+  for (int x = threadIdx.x; x < OWN * 64; x += blockDim.x) {
+    const int c = x & 3, i = (x >> 2) % OWN, r = x / (4 * OWN);
+    if (row0 + r >= row1 || nt0 + i >= ctiles) continue;
+    auto total = [&](int tile) {
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < nwaves; ++w)
+        sum += *reinterpret_cast<const f32x4 *>(red + ((w * NT + tile) * 64 + 16 * c + r) * 4);
+      return sum;
+    };
+    const int n = (nt0 + i) * 16 + 4 * c;
+    const size_t crow = static_cast<size_t>(row0 + r);
+    f32x4 v = total(i);
+    if constexpr (FORM == kGated) {
+      const f32x4 u = total(OWN + i);
+      const size_t inter = static_cast<size_t>(p.N >> 1);
+      if (p.GU) {
+        store4<OUT>(p.GU, crow * p.N + n, v);
+        store4<OUT>(p.GU, crow * p.N + inter + n, u);
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) v[z] = f8_gate(v[z], p.act) * u[z];
+      store4<OUT>(p.C, crow * inter + n, v);
+    } else {
+      if (p.bias) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z) v[z] += bits_to_f32_dyn(p.bias[static_cast<size_t>(e) * p.N + n + z], p.bias_dt);
+      }
+      store4<OUT>(p.C, crow * p.N + n, v);
+    }
+  }
+}
+
+namespace {
+
+constexpr int kMaxSlabs = 65535;   // grid.y
+
+template <int OUT, int NT, int FORM, bool BROW>
+hipError_t run_stream_as(const F8Problem &p, long slabs, hipStream_t s) {
+  const int nb = f8_blocks(p.K), waves = nb < 8 ? nb : 8;
+  const size_t lds = static_cast<size_t>(waves) * NT * 256 * sizeof(float);
+  const unsigned cols = FORM == kGated ? static_cast<unsigned>(((p.N >> 5) + NT / 2 - 1) / (NT / 2))
+                                       : static_cast<unsigned>(((p.N >> 4) + NT - 1) / NT);
+  if (static_cast<uint64_t>(cols) * 64 * waves > UINT32_MAX) return hipErrorNotSupported;
+  for (long s0 = 0; s0 < slabs; s0 += kMaxSlabs) {
+    const unsigned ny = static_cast<unsigned>(std::min<long>(slabs - s0, kMaxSlabs));
+    hipLaunchKernelGGL((k_f8_stream<OUT, NT, FORM, BROW>), dim3(cols, ny), dim3(64 * waves), lds, s, p,
+                       static_cast<int>(s0));
+  }
+  return hipGetLastError();
+}
+
+template <int OUT, int FORM, bool BROW>
+hipError_t run_stream(const F8Problem &p, hipStream_t s) {
+  // Row slabs: a grouped product has at most one partial slab per expert
+  // with rows.
+  const long slabs = FORM == kGrouped ? p.M / 16 + std::min(p.E, p.M) : (static_cast<long>(p.M) + 15) / 16;
+  return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+}
+
+template <int OUT>
+hipError_t run_f8(const F8Problem &p, const F8Args &a, hipStream_t s) {
+  if (a.gated) return run_stream<OUT, kGated, false>(p, s);
+  if (a.offsets) return run_stream<OUT, kGrouped, false>(p, s);
+  return a.b_block == 1 ? run_stream<OUT, kDense, true>(p, s) : run_stream<OUT, kDense, false>(p, s);
+}
+
+}  // namespace
+
+size_t f8_workspace_bytes(int m, int n, int k, int b_block) { return 0; }
+
+hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s) {
+  const F8Problem p{a.A, a.SA, a.B, a.SB, a.bias, a.C, a.GU, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, a.act};
+  switch (a.out) {
+    case QG_FP32: return run_f8<QG_FP32>(p, a, s);
+    case QG_FP16: return run_f8<QG_FP16>(p, a, s);
+    default: return run_f8<QG_BF16>(p, a, s);
+  }
+}
+
+}  // namespace qg

@@ -215,6 +215,59 @@ hipError_t launch_mx4_gemm(const Mx4Args &a, hipStream_t s);
 
 namespace qg {
 
+// Block-scaled 8-bit floats (F8).  hipErrorNotSupported: the sizes need more
+// threads than a launch has (2^32 - 1); nothing is enqueued.
+struct F8Quantize {
+  const void *X;            // [stack, rows, k] in dt
+  int stack, rows, k, dt;   // stack 1 by rows
+  int block;                // 1: a scale per row and 128 k; 128: per 128 x 128
+  uint8_t *Q;               // [stack, rows, k], or null
+  float *S;
+  uint8_t *QT;              // [stack, k, rows padded to 16], or null
+  float *ST;
+};
+hipError_t launch_quantize_f8(const F8Quantize &q, hipStream_t s);
+hipError_t launch_dequant_f8(const uint8_t *Q, const float *S, void *out, int stack, int rows, int k, int block,
+                             int out_dt, hipStream_t s);
+
+struct F8Args {
+  const uint8_t *A;         // [M, K] codes
+  const float *SA;          // [blocks of K, M]
+  const uint8_t *B;         // [N, K] codes (per expert)
+  const float *SB;          // [blocks of N, blocks of K] (per expert), or [blocks of K, N]
+  int b_block;              // 128 or 1
+  const uint16_t *bias;     // [N] (per expert) or null
+  void *C;                  // [M, N] in `out`; gated [M, N / 2]
+  int M, N, K;
+  int out, bias_dt;
+  const int32_t *offsets;   // grouped: [E + 1] row offsets, else null
+  int E;                    // grouped: experts
+  bool gated;               // B = [gate; up] channels
+  int act;                  // gated: qg_gate
+  void *GU;                 // gated: [M, N] in `out`, or null
+  void *ws;                 // K slices' partials, may be null
+  size_t ws_bytes;
+};
+size_t f8_workspace_bytes(int m, int n, int k, int b_block);
+hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s);
+
+// Gradient of H = act(g) * u, quantized by rows (D) and transposed (DT).
+struct F8GatedGrad {
+  const void *dH, *GU;      // [m, inter], [m, 2 inter] in dt
+  int m, inter, dt, act;
+  uint8_t *D;               // [m, 2 inter], or null
+  float *SD;                // [2 inter / 128, m]
+  uint8_t *DT;              // [2 inter, m padded to 16], or null
+  float *SDT;               // [blocks of m, 2 inter]
+};
+hipError_t launch_gated_f8_grad(const F8GatedGrad &g, hipStream_t s);
+// Zeros (a kernel: it may be captured), a multiple of 16 bytes.
+hipError_t launch_fill_zero(void *p, size_t bytes, hipStream_t s);
+
+}  // namespace qg
+
+namespace qg {
+
 // Streaming-read probe (measurement).
 size_t read_probe_blocks(size_t bytes);
 hipError_t launch_read_probe(const void *buf, size_t bytes, uint32_t *out, hipStream_t s);
