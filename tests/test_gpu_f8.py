@@ -11,6 +11,7 @@ import weight_only_quantized_w8a16_amd as qg
 pytestmark = pytest.mark.gpu
 
 BF, HF, SF = torch.bfloat16, torch.float16, torch.float32
+TILES = ["auto", "stream", "T256", "T256N", "T128", "T64"]
 
 
 def dev(a):
@@ -183,7 +184,9 @@ def close(got, want, tol):
 @pytest.mark.parametrize("m,n,k", SHAPES)
 @pytest.mark.parametrize("b_block", [128, 1])
 @pytest.mark.parametrize("dtype", [BF, HF, SF])
-def test_gemm(m, n, k, b_block, dtype):
+@pytest.mark.parametrize("tile", TILES)
+def test_gemm(m, n, k, b_block, dtype, tile):
+    qg.set_override(f8_tile=tile)
     rng = np.random.default_rng(m * 7 + n + k)
     for make, biased in ((exact_pair, False), (exact_pair, True), (random_pair, True)):
         (ca, sa), (cb, sb) = make(rng, m, k, 1), make(rng, n, k, b_block)
@@ -198,6 +201,38 @@ def test_gemm(m, n, k, b_block, dtype):
         else:
             tol = sum_bound(a, b, k) + 2.0 ** -24 * np.abs(want)
             close(got, want, tol + half_step(dtype) * (np.abs(want) + tol))
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 48, 272), (130, 272, 1040), (300, 528, 2064)])
+@pytest.mark.parametrize("split", [2, 3, 5, 100])
+@pytest.mark.parametrize("tile", TILES[2:])
+def test_gemm_in_k_slices(m, n, k, split, tile):
+    qg.set_override(f8_tile=tile, f8_split=split)
+    rng = np.random.default_rng(split)
+    for b_block, dtype in ((128, BF), (1, SF)):
+        (ca, sa), (cb, sb) = exact_pair(rng, m, k, 1), exact_pair(rng, n, k, b_block)
+        bias = torch.from_numpy(rng.integers(-8, 9, n) / 4.0).to(BF)
+        want = ref.values(ca, sa) @ ref.values(cb, sb, b_block).T + bias.double().numpy()
+        args = dict(bias=bias.cuda(), out_dtype=dtype, b_block=b_block)
+        assert qg.f8_workspace_size(m, n, k, b_block) >= 2 * m * n * 4
+        same(qg.gemm_f8(codes8(ca), dev(sa), codes8(cb), dev(sb), **args), want)
+        none = torch.empty(0, dtype=torch.uint8, device="cuda")
+        same(qg.gemm_f8(codes8(ca), dev(sa), codes8(cb), dev(sb), workspace=none, **args), want)
+
+
+@pytest.mark.parametrize("tile", TILES[2:])
+def test_gemm_many_tiles_a_workgroup(tile):
+    # more tiles than workgroups, an odd number of steps: the stream of steps crosses tile borders
+    qg.set_override(f8_tile=tile)
+    rng = np.random.default_rng(0)
+    m, n, k = (2100, 9232, 400) if tile == "T256" else (1100, 9232, 400)
+    (ca, sa), (cb, sb) = exact_pair(rng, m, k, 1), exact_pair(rng, n, k, 128)
+    a, b = dev(ref.values(ca, sa)), dev(ref.values(cb, sb, 128))
+    args = (codes8(ca), dev(sa), codes8(cb), dev(sb))
+    want = (a.double() @ b.double().t()).float()
+    for dtype in (BF, SF):
+        for _ in range(3):
+            assert torch.equal(qg.gemm_f8(*args, out_dtype=dtype), want.to(dtype))
 
 
 def test_gemm_out_and_workspace_given():
@@ -224,7 +259,9 @@ def test_gemm_no_rows_and_no_channels():
 
 @pytest.mark.parametrize("m", [3, 40, 300])
 @pytest.mark.parametrize("b_block", [128, 1])
-def test_nan_reaches_its_own_outputs_only(m, b_block):
+@pytest.mark.parametrize("tile", TILES)
+def test_nan_reaches_its_own_outputs_only(m, b_block, tile):
+    qg.set_override(f8_tile=tile)
     # a NaN scale, and NaN codes next to the ends of rows whose last block is short
     rng = np.random.default_rng(m)
     n, k = 144, 272
@@ -245,7 +282,9 @@ def test_nan_reaches_its_own_outputs_only(m, b_block):
     ([3, 0, 1, 17], 0, 0), ([0, 0, 5], 2, 3), ([40, 130, 0, 7], 0, 9), ([1] * 70, 1, 0), ([0, 300, 0], 0, 0),
     ([0, 0], 4, 0), ([16, 128, 64, 32], 0, 0),
 ])
-def test_grouped(sizes, before, behind, dtype):
+@pytest.mark.parametrize("tile", TILES)
+def test_grouped(sizes, before, behind, dtype, tile):
+    qg.set_override(f8_tile=tile)
     rng = np.random.default_rng(len(sizes) + sum(sizes))
     E, n, k = len(sizes), 144, 400
     off = np.concatenate([[0], np.cumsum(sizes)]) + before
@@ -267,7 +306,9 @@ def test_grouped(sizes, before, behind, dtype):
 
 
 @pytest.mark.parametrize("off", [[0, 9, 4, 12], [-5, 3, 40, 7], [12, 0, 12, 12], [2 ** 31 - 1, -2 ** 31, 0, 12]])
-def test_grouped_offsets_out_of_order_stay_inside(off):
+@pytest.mark.parametrize("tile", TILES)
+def test_grouped_offsets_out_of_order_stay_inside(off, tile):
+    qg.set_override(f8_tile=tile)
     # what they mean is unspecified; no row outside is written
     rng = np.random.default_rng(1)
     ca, sa = exact_pair(rng, 12, 144, 1)
@@ -290,7 +331,9 @@ def small_pair(rng, rows, k, block, size):
                                        (300, 256, 528)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", [BF, HF, SF])
-def test_gated(m, inter, k, act, dtype):
+@pytest.mark.parametrize("tile", TILES)
+def test_gated(m, inter, k, act, dtype, tile):
+    qg.set_override(f8_tile=tile)
     rng = np.random.default_rng(m + inter + k)
     (ca, sa), (cb, sb) = small_pair(rng, m, k, 1, 1.0), small_pair(rng, 2 * inter, k, 128, 2.0 / np.sqrt(k))
     a, b = ref.values(ca, sa), ref.values(cb, sb, 128)
@@ -347,7 +390,9 @@ def quantised_gradient(d, near):
 @pytest.mark.parametrize("m,inter,k", [(1, 128, 16), (16, 128, 272), (35, 256, 144), (130, 384, 272), (300, 128, 528)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", [BF, HF])
-def test_gated_backward(m, inter, k, act, dtype):
+@pytest.mark.parametrize("tile", ["auto", "stream", "T256", "T64"])
+def test_gated_backward(m, inter, k, act, dtype, tile):
+    qg.set_override(f8_tile=tile)
     rng = np.random.default_rng(m + inter + k)
     x = rng.standard_normal((m, k))
     w = rng.standard_normal((2 * inter, k)) * 0.1

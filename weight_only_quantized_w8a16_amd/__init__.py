@@ -118,8 +118,8 @@ _override: dict = {}
 
 def set_override(**choices) -> None:
     """Force dispatch choices for later calls (qg_set_override): path,
-    prefill_tile, splitk, moe_tile, w8a8_tile, w8a8_split, mx4_tile, mx4_split.  Merges with the
-    choices set before; a value of None returns that key to automatic."""
+    prefill_tile, splitk, moe_tile, w8a8_tile, w8a8_split, mx4_tile, mx4_split,
+    f8_tile, f8_split.  Merges with the choices set before; a value of None returns that key to automatic."""
     for key, val in choices.items():
         if val is None:
             _override.pop(key, None)

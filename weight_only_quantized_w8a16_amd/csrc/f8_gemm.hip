@@ -21,25 +21,12 @@
 #include <algorithm>
 
 #include "f8_common.hpp"
+#include "f8_tile.hpp"
 #include "row_groups.hpp"
 
 namespace qg {
 
 namespace {
-
-enum { kDense, kGrouped, kGated };   // forms
-
-struct F8Problem {
-  const uint8_t *A;
-  const float *SA;
-  const uint8_t *B;
-  const float *SB;
-  const uint16_t *bias;
-  void *C, *GU;
-  int M, N, K, bias_dt;   // N: channels of B, gate and up ones alike
-  const int32_t *offsets;
-  int E, act;
-};
 
 template <int OUT>
 __device__ __forceinline__ void store4(void *C, size_t off, f32x4 v) {
@@ -179,6 +166,22 @@ __global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
   }
 }
 
+// K slices: C = RNE_out(the slices' partials summed in slice order + bias).
+template <int OUT>
+__global__ __launch_bounds__(256) void k_f8_reduce(F8Problem p) {
+  const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
+  for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < mn; i += step) {
+    f32x4 v = *reinterpret_cast<const f32x4 *>(p.part + i);
+    for (int sl = 1; sl < p.slices; ++sl) v += *reinterpret_cast<const f32x4 *>(p.part + sl * mn + i);
+    const int col = static_cast<int>(i % p.N);
+    if (p.bias) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] += bits_to_f32_dyn(p.bias[col + x], p.bias_dt);
+    }
+    store4<OUT>(p.C, i, v);
+  }
+}
+
 namespace {
 
 constexpr int kMaxSlabs = 65535;   // grid.y
@@ -206,23 +209,120 @@ hipError_t run_stream(const F8Problem &p, hipStream_t s) {
   return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
 }
 
+// The tiles, in the order qg_set_override names them.
+template <int TILE, bool BROW, bool GATED> struct F8Tiling;
+template <bool BROW, bool GATED> struct F8Tiling<kF8T256, BROW, GATED> { using Eng = F8Engine<256, 256, 2, 4, 2, BROW, GATED>; };
+template <bool BROW, bool GATED> struct F8Tiling<kF8T256N, BROW, GATED> { using Eng = F8Engine<128, 256, 2, 4, 2, BROW, GATED>; };
+template <bool BROW, bool GATED> struct F8Tiling<kF8T128, BROW, GATED> { using Eng = F8Engine<128, 128, 2, 2, 2, BROW, GATED>; };
+template <bool BROW, bool GATED> struct F8Tiling<kF8T64, BROW, GATED> { using Eng = F8Engine<64, 128, 2, 2, 2, BROW, GATED>; };
+
+// 32-bit offsets of the tile kernels stay below this.
+constexpr uint64_t kF8Span = uint64_t(1) << 31;
+
+struct F8Plan {
+  int tile;            // F8Kernel
+  int kseg, slices;    // K slices in steps
+  size_t bytes;        // partials
+};
+
+F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
+  const int steps = f8_blocks(K);
+  F8Plan pl{kF8Stream, steps, 1, 0};
+  const Override ov = dispatch_override();
+  // The tile kernels' offsets span a tile's rows of A, B and C (or partials),
+  // and an expert's scales.
+  const uint64_t nb = f8_blocks(N);
+  if (uint64_t(256) * 4 * N >= kF8Span || uint64_t(256) * K >= kF8Span || nb * steps * 4 >= kF8Span) return pl;
+  if (ov.f8_tile >= 0) pl.tile = ov.f8_tile;
+  else if (M > 16) pl.tile = M > 1024 ? kF8T256 : M > 128 ? kF8T128 : kF8T64;
+  if (pl.tile == kF8Stream || form != kDense) return pl;
+  if (ov.f8_split > 0) {
+    const int want = std::min(ov.f8_split, steps);
+    pl.kseg = (steps + want - 1) / want;
+    pl.slices = (steps + pl.kseg - 1) / pl.kseg;
+  }
+  if (pl.slices > 1) pl.bytes = static_cast<size_t>(pl.slices) * M * N * sizeof(float);
+  return pl;
+}
+
+// Workgroups of `Eng` a CU holds: by LDS, and by registers.
+template <class Eng>
+constexpr int groups_per_cu() {
+  const int lds = 160 * 1024 / (Eng::NS * Eng::STAGE + Eng::EP), waves = 4 * Eng::WAVES / Eng::NW;
+  return std::max(1, std::min(lds, waves));
+}
+
 template <int OUT>
-hipError_t run_f8(const F8Problem &p, const F8Args &a, hipStream_t s) {
-  if (a.gated) return run_stream<OUT, kGated, false>(p, s);
-  if (a.offsets) return run_stream<OUT, kGrouped, false>(p, s);
-  return a.b_block == 1 ? run_stream<OUT, kDense, true>(p, s) : run_stream<OUT, kDense, false>(p, s);
+hipError_t reduce_f8(const F8Problem &p, hipStream_t s) {
+  const size_t blocks = (static_cast<size_t>(p.M) * p.N / 4 + 255) / 256;
+  hipLaunchKernelGGL(k_f8_reduce<OUT>, dim3(static_cast<unsigned>(std::min<size_t>(blocks, 65536))), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+template <class Eng, class Store, class Work>
+hipError_t run_tiles_as(const F8Problem &p, int form, hipStream_t s) {
+  const int64_t tn = ((form == kGated ? p.N / 2 : p.N) + Eng::COLS - 1) / Eng::COLS;
+  // A grouped product has at most one partial row tile per expert with rows.
+  const int64_t tm = form == kGrouped ? p.M / Eng::BM + std::min(p.E, p.M) : (p.M + Eng::BM - 1) / Eng::BM;
+  const int64_t items = tm * tn * p.slices;
+  if (items > INT32_MAX / 2) return hipErrorNotSupported;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, device_cus() * groups_per_cu<Eng>()));
+  hipLaunchKernelGGL((k_f8_tiles<Eng, Store, Work>), dim3(grid), dim3(Eng::NTHR), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int OUT, int FORM, bool BROW, int TILE>
+hipError_t run_tiles(const F8Problem &p, hipStream_t s) {
+  using Eng = typename F8Tiling<TILE, BROW, FORM == kGated>::Eng;
+  if constexpr (FORM == kGated) {
+    return p.GU ? run_tiles_as<Eng, F8StoreGated<OUT, true>, F8DenseWork<Eng>>(p, FORM, s)
+                : run_tiles_as<Eng, F8StoreGated<OUT, false>, F8DenseWork<Eng>>(p, FORM, s);
+  } else if constexpr (FORM == kGrouped) {
+    return run_tiles_as<Eng, F8Store<OUT, false>, F8GroupWork<Eng>>(p, FORM, s);
+  } else {
+    if (p.slices == 1) return run_tiles_as<Eng, F8Store<OUT, false>, F8DenseWork<Eng>>(p, FORM, s);
+    const hipError_t e = run_tiles_as<Eng, F8Store<OUT, true>, F8DenseWork<Eng>>(p, FORM, s);
+    return e == hipSuccess ? reduce_f8<OUT>(p, s) : e;
+  }
+}
+
+template <int OUT, int FORM, bool BROW>
+hipError_t run_form(const F8Problem &p, int tile, hipStream_t s) {
+  switch (tile) {
+    case kF8T256: return run_tiles<OUT, FORM, BROW, kF8T256>(p, s);
+    case kF8T256N: return run_tiles<OUT, FORM, BROW, kF8T256N>(p, s);
+    case kF8T128: return run_tiles<OUT, FORM, BROW, kF8T128>(p, s);
+    case kF8T64: return run_tiles<OUT, FORM, BROW, kF8T64>(p, s);
+    default: return run_stream<OUT, FORM, BROW>(p, s);
+  }
+}
+
+template <int OUT>
+hipError_t run_f8(const F8Problem &p, int form, bool brow, int tile, hipStream_t s) {
+  if (form == kGated) return run_form<OUT, kGated, false>(p, tile, s);
+  if (form == kGrouped) return run_form<OUT, kGrouped, false>(p, tile, s);
+  return brow ? run_form<OUT, kDense, true>(p, tile, s) : run_form<OUT, kDense, false>(p, tile, s);
 }
 
 }  // namespace
 
-size_t f8_workspace_bytes(int m, int n, int k, int b_block) { return 0; }
+size_t f8_workspace_bytes(int m, int n, int k, int b_block) { return plan_f8(m, n, k, b_block == 1, kDense, 0).bytes; }
 
 hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s) {
-  const F8Problem p{a.A, a.SA, a.B, a.SB, a.bias, a.C, a.GU, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, a.act};
+  const int form = a.gated ? kGated : a.offsets ? kGrouped : kDense;
+  const bool brow = a.b_block == 1;
+  const F8Plan pl = plan_f8(a.M, a.N, a.K, brow, form, a.E);
+  F8Problem p{a.A, a.SA, a.B, a.SB, a.bias, a.C, a.GU, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, a.act,
+              nullptr, f8_blocks(a.K), 1};
+  if (pl.slices > 1 && a.ws && a.ws_bytes >= pl.bytes) {
+    p.part = static_cast<float *>(a.ws);
+    p.kseg = pl.kseg;
+    p.slices = pl.slices;
+  }
   switch (a.out) {
-    case QG_FP32: return run_f8<QG_FP32>(p, a, s);
-    case QG_FP16: return run_f8<QG_FP16>(p, a, s);
-    default: return run_f8<QG_BF16>(p, a, s);
+    case QG_FP32: return run_f8<QG_FP32>(p, form, brow, pl.tile, s);
+    case QG_FP16: return run_f8<QG_FP16>(p, form, brow, pl.tile, s);
+    default: return run_f8<QG_BF16>(p, form, brow, pl.tile, s);
   }
 }
 

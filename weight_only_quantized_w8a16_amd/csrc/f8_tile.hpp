@@ -1,0 +1,567 @@
+// f8_tile.hpp -- tiled products of block-scaled 8-bit floats (F8) on gfx950, for
+// many rows: a fixed set of workgroups walks the output tiles (BM rows x BN
+// channels), 128 k -- one block of scales -- a step, and the steps of all of a
+// workgroup's tiles form one stream.
+//
+// Per step the operands' bytes and scales go from global memory straight into
+// one of NS LDS stages (buffer_load ... lds), NS steps ahead of use and across
+// tile borders.  Each wave waits for its own loads of the next step and meets
+// the others at one barrier a step, when three quarters (or all but two row tiles)
+// of the step are multiplied and all of it is in registers.  What is left
+// multiplies while the next step's first fragments are read.
+//
+// A stage holds BM rows of A and BN rows of B, 128 bytes each, 16-byte chunk c
+// of row r at chunk c ^ ((r / 2) % 8): 16 lanes reading one chunk of 16 rows touch 16
+// distinct 16-byte bank groups (the swizzle is applied on the source side of the
+// load), then the step's BM + BN scales.  Rows and channels past the last one,
+// and chunks past K, read as zeros; their outputs are not stored.
+//
+// Gated tiles hold BN / 2 gate channels and the BN / 2 up channels beside them: of a
+// wave's WTN channels the first half are gate ones, so a lane has both sums of
+// each of its outputs.
+#pragma once
+
+#include <type_traits>
+#include <utility>
+
+#include "f8_common.hpp"
+#include "mx4_tile.hpp"
+#include "row_groups.hpp"
+
+namespace qg {
+
+enum { kDense, kGrouped, kGated };   // forms of a product
+
+struct F8Problem {
+  const uint8_t *A;
+  const float *SA;
+  const uint8_t *B;
+  const float *SB;
+  const uint16_t *bias;
+  void *C, *GU;
+  int M, N, K, bias_dt;   // N: channels of B, gate and up ones alike
+  const int32_t *offsets;
+  int E, act;
+  float *part;            // K slices: fp32 partial sums [slices, M, N], else null
+  int kseg, slices;       // steps per slice, slices
+};
+
+// One tile: rows [row_lo, row_last] of A and C, channels (gated: gate channels)
+// from col_lo on, of expert e; steps [s0, s1).
+struct F8Item {
+  int row_lo, row_last, col_lo, e, slice, s0, s1;
+  const float *scales;    // of the wave's scale load (F8Engine::prepare)
+  uint32_t scale_bytes;
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int NS_, bool BROW_, bool GATED_>
+struct F8Engine {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr bool BROW = BROW_, GATED = GATED_;
+  static constexpr int NW = WM * WN, NTHR = 64 * NW;
+  static constexpr int WTM = BM / WM, WTN = BN / WN;   // wave tile
+  static constexpr int TM = WTM / 16, TN = WTN / 16;   // 16x16 accumulators per wave
+  static constexpr int RP = TM / 2;                    // pairs of row tiles
+  static constexpr int COLS = GATED ? BN / 2 : BN;     // columns of C a tile
+  static constexpr int A_DMA = BM / 8 / NW, B_DMA = BN / 8 / NW;   // 1 KiB loads (8 rows) a wave and step
+  static constexpr int S_LOADS = (BM + BN) / 64;       // 64 scales, a load a wave
+  static constexpr int STAGE_A = BM * 128, STAGE_S = STAGE_A + BN * 128, STAGE = STAGE_S + (BM + BN) * 4;
+  static constexpr int LOADS = A_DMA + B_DMA + 1;
+  static constexpr int WAVES = 2;   // a SIMD
+  static constexpr int EP_ROWS = 16, EP = NW * EP_ROWS * WTN * 2;
+  static_assert(TM % 2 == 0 && TN % 2 == 0 && WTN <= 128 && 128 % (GATED ? WTN / 2 : WTN) == 0, "tile shape");
+  static_assert(A_DMA % 2 == 0 && B_DMA % 2 == 0 && (A_DMA * NW * 8 == BM) && (B_DMA * NW * 8 == BN), "row loads");
+  static_assert(S_LOADS <= NW && (COLS % 128 == 0 || 128 % COLS == 0), "scale loads");
+  static_assert(RP % 2 == 0 || NS % 2 == 0, "fragment buffers in step with the stages");
+  static_assert(NS * STAGE + EP <= 160 * 1024, "LDS");
+
+  const F8Problem &p;
+  const int lane, wave, wm, wn, nl, q, kb;
+  uint32_t lane_off[2];
+  int chunk[2], a_addr[2], b_addr[2];
+  uint32_t scale_at, scale_step, scale_cut;   // a lane's byte offset; bytes from step to step, and of these off the end
+  f32x4 acc[TM][TN];
+
+  __device__ __forceinline__ F8Engine(const F8Problem &pr, int wave_)
+      : p(pr), lane(threadIdx.x & 63), wave(wave_), wm(wave / WN), wn(wave % WN), nl(lane & 15), q(lane >> 4),
+        kb(f8_blocks(pr.K)) {
+    // Load i of a wave brings 8 rows, lane l row l / 8, placed chunk l % 8.
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      chunk[x] = ((lane & 7) ^ ((4 * x + (lane >> 4)) & 7)) << 4;
+      lane_off[x] = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.K) + chunk[x];
+      a_addr[x] = (wm * WTM + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
+      b_addr[x] = STAGE_A + (wn * WTN + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
+    }
+    // 64 scales a wave and step: of 64 rows of A or, behind them, channels of B.
+    // With fewer such loads than waves, waves repeat one (the same values to the
+    // same place).
+    const int r = scale_load() * 64 + lane;
+    if (r < BM) {
+      scale_at = static_cast<uint32_t>(r) * 4u;
+      scale_step = static_cast<uint32_t>(p.M) * 4u;
+    } else if (BROW) {
+      scale_at = static_cast<uint32_t>(r - BM) * 4u;
+      scale_step = static_cast<uint32_t>(p.N) * 4u;
+    } else {
+      scale_at = static_cast<uint32_t>(channel(0, r - BM) >> 7) * static_cast<uint32_t>(kb) * 4u;
+      scale_step = 4u;
+    }
+    scale_step = __builtin_amdgcn_readfirstlane(scale_step);
+    scale_cut = scale_load() < BM / 64 || BROW ? 0u : 4u;
+  }
+  __device__ __forceinline__ int scale_load() const { return wave % S_LOADS; }
+  // What a tile's scale loads start from.  (col_lo + r) / 128 = col_lo / 128 + r / 128
+  // for the tile's channels: its columns are a part of 128 or a multiple.
+  __device__ __forceinline__ void prepare(F8Item &t) const {
+    if (scale_load() < BM / 64) {
+      t.scales = p.SA + t.row_lo;
+      t.scale_bytes = static_cast<uint32_t>(t.row_last - t.row_lo + 1) * 4u;
+    } else if (BROW) {
+      t.scales = p.SB + t.col_lo;
+      t.scale_bytes = static_cast<uint32_t>(p.N - t.col_lo) * 4u;
+    } else {
+      const uint32_t nb = f8_blocks(p.N), c0 = static_cast<uint32_t>(t.col_lo >> 7);
+      t.scales = p.SB + (static_cast<size_t>(t.e) * nb + c0) * kb;
+      t.scale_bytes = (nb - c0) * static_cast<uint32_t>(kb) * 4u;
+    }
+  }
+
+  static constexpr uint32_t kOutside = 0x80000000u;   // past every resource
+
+  // Channel of row r of a tile's part of B, the tile's columns from col_lo on.
+  __device__ __forceinline__ int channel(int col_lo, int r) const {
+    if constexpr (GATED) {
+      constexpr int H = WTN / 2;
+      const int w = r / WTN, in = r % WTN;
+      return col_lo + w * H + in % H + (in >= H ? p.N >> 1 : 0);
+    } else {
+      return col_lo + r;
+    }
+  }
+
+  __device__ __forceinline__ void issue(char *stage, const F8Item &t, int step) const {
+    const uint32_t K = static_cast<uint32_t>(p.K);
+    const int rem = p.K - step * 128;   // bytes of the rows left
+    uint32_t off[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) off[x] = chunk[x] < rem ? lane_off[x] : kOutside;
+    const int rows = t.row_last - t.row_lo + 1, chans = GATED ? COLS : min(BN, p.N - t.col_lo);
+    // A resource for each load, over the rows from its first on that are left: the
+    // lanes' offsets are the same for all (scalar work instead of registers).
+    auto rsrc = [&](const uint8_t *first, int left) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t *>(first), 0,
+          static_cast<int>(left > 0 ? static_cast<uint32_t>(left) * K - static_cast<uint32_t>(step) * 128u : 0u), kRsrcFlags);
+    };
+    const uint8_t *A = p.A + static_cast<size_t>(t.row_lo) * K + static_cast<size_t>(step) * 128;
+#pragma unroll
+    for (int i = 0; i < A_DMA; ++i) {
+      const int row = wave * A_DMA + i;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(A + static_cast<size_t>(8 * row) * K, rows - 8 * row),
+                                               lds_ptr(stage + row * 1024), 16, static_cast<int>(off[i & 1]), 0, 0, 0);
+    }
+    const uint8_t *B = p.B + static_cast<size_t>(t.e) * p.N * K + static_cast<size_t>(step) * 128;
+#pragma unroll
+    for (int i = 0; i < B_DMA; ++i) {
+      const int row = wave * B_DMA + i;   // gated tiles have all of their channels
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc(B + static_cast<size_t>(channel(t.col_lo, 8 * row)) * K, GATED ? 8 : chans - 8 * row),
+          lds_ptr(stage + STAGE_A + row * 1024), 16, static_cast<int>(off[i & 1]), 0, 0, 0);
+    }
+    const auto rS = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char *>(reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step), 0,
+        static_cast<int>(t.scale_bytes - static_cast<uint32_t>(step) * scale_cut), kRsrcFlags);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, lds_ptr(stage + STAGE_S + scale_load() * 256), 4,
+                                             static_cast<int>(scale_at), 0, 0, 0);
+  }
+
+  // acc[i][j]: lane (nl, q) holds row 16 i + nl, columns 16 j + 4 q .. + 3.
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // B's scales of a step: per four columns, or one (gated: two) for the wave.
+  struct ScalesB {
+    std::conditional_t<BROW, f32x4, float> s[BROW ? TN : GATED ? 2 : 1];
+  };
+  struct Frags {
+    i32x8 a[2][2], b[TN];
+    float sa[2][2];
+    ScalesB sb;
+  };
+  __device__ __forceinline__ i32x8 read(const char *stage, const int (&addr)[2], int i) const {
+    return f8_frag(*reinterpret_cast<const u32x4 *>(stage + addr[0] + 2048 * i),
+                   *reinterpret_cast<const u32x4 *>(stage + addr[1] + 2048 * i));
+  }
+  __device__ __forceinline__ void read_a(const char *stage, int rp, i32x8 (&a)[2], float (&sa)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[h] = read(stage, a_addr, 2 * rp + h);
+      sa[h] = *reinterpret_cast<const float *>(stage + STAGE_S + (wm * WTM + 16 * (2 * rp + h) + nl) * 4);
+    }
+  }
+  __device__ __forceinline__ ScalesB read_sb(const char *stage) const {
+    ScalesB s;
+    const char *at = stage + STAGE_S + (BM + wn * WTN) * 4;
+    if constexpr (BROW) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) s.s[j] = *reinterpret_cast<const f32x4 *>(at + (16 * j + 4 * q) * 4);
+    } else {
+      s.s[0] = *reinterpret_cast<const float *>(at);
+      if constexpr (GATED) s.s[1] = *reinterpret_cast<const float *>(at + WTN * 2);
+    }
+    return s;
+  }
+  __device__ __forceinline__ void apply(const f32x4 (&t)[2], int rp, int j, const float (&sa)[2], const ScalesB &sb) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 &c = acc[2 * rp + h][j];
+      if constexpr (BROW) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c[v] += t[h][v] * (sa[h] * sb.s[j][v]);
+      } else {
+        const float s = sa[h] * sb.s[GATED && j >= TN / 2 ? 1 : 0];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c[v] += t[h][v] * s;
+      }
+    }
+  }
+  // The first fragments of a step.
+  template <int X>
+  __device__ __forceinline__ void head(const char *stage, Frags &f) const {
+    read_a(stage, 0, f.a[X], f.sa[X]);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) f.b[j] = read(stage, b_addr, j);
+    f.sb = read_sb(stage);
+  }
+  // Which half of f.a step I of the stages starts on.
+  static constexpr int start(int I) { return RP % 2 ? I & 1 : 0; }
+  // One step, its first fragments read; `meet` waits for the next stage and gives
+  // this one up.  Two row tiles by one column tile at a time (two matrix instructions),
+  // the sums of the two before applied meanwhile.
+  template <int X0, class Meet>
+  __device__ __forceinline__ void step(const char *stage, const char *next, Frags &f, Meet &&meet) {
+    f32x4 t[2][2];
+    float ts[2][2];   // the scales of t's rows
+    [[maybe_unused]] ScalesB sb;
+#pragma unroll
+    for (int g = 0; g < RP * TN; ++g) {
+      const int rp = g / TN, j = g % TN, x = (X0 + rp) & 1;
+      if (j == 0) {
+        if (rp < RP - 1) {
+          read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
+        } else {
+          meet();
+          read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
+          if constexpr (!BROW) sb = read_sb(next);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        t[g & 1][h] = f8_mfma(f.b[j], f.a[x][h]);
+        ts[g & 1][h] = f.sa[x][h];
+      }
+      if (rp == RP - 1) f.b[j] = read(next, b_addr, j);
+      if (g) apply(t[(g - 1) & 1], (g - 1) / TN, (g - 1) % TN, ts[(g - 1) & 1], f.sb);
+      __builtin_amdgcn_sched_barrier(0);   // one group's results in registers besides the next's
+    }
+    apply(t[(RP * TN - 1) & 1], RP - 1, TN - 1, ts[(RP * TN - 1) & 1], f.sb);
+    // With scales by rows of B (four a column tile) the next step's take the place
+    // of this one's, for want of registers.
+    if constexpr (BROW) f.sb = read_sb(next);
+    else f.sb = sb;
+  }
+
+  // 16-bit results: lane rows q trade with their neighbours across a pair of
+  // column tiles, so a lane holds eight consecutive columns (16 bytes) of its
+  // row -- q = 0, 2 those of the first tile, q = 1, 3 of the second -- and 16 rows
+  // at a time go through the wave's LDS area to be stored in whole row pieces.
+  // Tiles j0 .. j0 + n - 1 of row tile i, to columns from col0 on.
+  template <int N_, class Out, class Value>
+  __device__ __forceinline__ void store_row(const Out &out, char *ep, int ln, int i, int col0, Value &&value) const {
+    const int r0 = wm * WTM + 16 * i, nl = ln & 15, q = ln >> 4;
+    const Mx4RowBuffer<N_ * 32, EP_ROWS> buf{ep + wave * (EP_ROWS * WTN * 2)};
+#pragma unroll
+    for (int j = 0; j < N_; j += 2) {
+      const f32x4 x = value(j), y = value(j + 1);
+      if constexpr (Out::kBytes == 4) {
+        out.put4(r0 + nl, col0 + 16 * j + 4 * q, x);
+        out.put4(r0 + nl, col0 + 16 * j + 16 + 4 * q, y);
+      } else {
+        const uint32_t x0 = pack2<Out::kType>(x[0], x[1]), x1 = pack2<Out::kType>(x[2], x[3]);
+        const uint32_t y0 = pack2<Out::kType>(y[0], y[1]), y1 = pack2<Out::kType>(y[2], y[3]);
+        const auto lo = __builtin_amdgcn_permlane16_swap(x0, y0, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(x1, y1, false, false);
+        buf.write(nl, 2 * j + 2 * (q & 1) + (q >> 1), u32x4{lo[0], hi[0], lo[1], hi[1]});
+      }
+    }
+    if constexpr (Out::kBytes == 2) buf.drain(out, r0, col0, ln);
+  }
+  // The lane, as a value that is not known before the tile's end: what the results'
+  // addresses take from it would else be kept in registers through the steps.
+  __device__ __forceinline__ int late_lane() const {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  }
+};
+
+// Rows of a result: `cols` columns in a row of N, through a buffer resource over
+// the tile's rows, so that rows past its last one are not stored, nor columns
+// past `cols`, and every wave issues the same number of stores.
+template <int OUT>
+struct F8Rows {
+  static constexpr int kType = OUT, kBytes = OUT == QG_FP32 ? 4 : 2;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int stride, cols;
+  __device__ __forceinline__ F8Rows(void *base, const F8Item &t, int stride_, int cols_) : stride(stride_), cols(cols_) {
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        static_cast<char *>(base) + static_cast<size_t>(t.row_lo) * stride * kBytes, 0,
+        static_cast<int>(static_cast<uint32_t>(t.row_last - t.row_lo + 1) * static_cast<uint32_t>(stride) * kBytes), kRsrcFlags);
+  }
+  __device__ __forceinline__ int offset(int r, int col) const {
+    const uint32_t off = (static_cast<uint32_t>(r) * static_cast<uint32_t>(stride) + static_cast<uint32_t>(col)) * kBytes;
+    return static_cast<int>(col < cols ? off : 0xFFFFFFF0u);
+  }
+  __device__ __forceinline__ void put4(int r, int col, f32x4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, offset(r, col), 0, 0);
+  }
+  __device__ __forceinline__ void put8(int r, int col, u32x4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, offset(r, col), 0, kNonTemporal);
+  }
+};
+
+// Where a tile's sums go: C with the bias added in fp32, or, unrounded, a K
+// slice's partials, or through the gate.  stores(): a wave's stores of a tile.
+template <int OUT, bool SPLIT>
+struct F8Store {
+  static constexpr int kOut = SPLIT ? QG_FP32 : OUT;
+  template <class Eng>
+  static constexpr int stores() { return Eng::TM * Eng::TN * 4 * F8Rows<kOut>::kBytes / 16; }
+  template <class Eng>
+  static __device__ __forceinline__ void run(Eng &eng, const F8Problem &p, const F8Item &t, char *ep) {
+    const F8Rows<kOut> rows(SPLIT ? p.part + static_cast<size_t>(t.slice) * p.M * p.N : p.C, t, p.N, p.N);
+    const int col0 = t.col_lo + eng.wn * Eng::WTN, ln = eng.late_lane();
+    f32x4 bias[Eng::TN];
+#pragma unroll
+    for (int j = 0; j < Eng::TN; ++j) {
+      bias[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (!SPLIT && p.bias) {
+        const int c = min(col0 + 16 * j + 4 * (ln >> 4), p.N - 4);   // columns past N are not stored
+        const uint16_t *b = p.bias + static_cast<size_t>(t.e) * p.N + c;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) bias[j][v] = bits_to_f32_dyn(b[v], p.bias_dt);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Eng::TM; ++i) {
+      eng.template store_row<Eng::TN>(rows, ep, ln, i, col0, [&](int j) {
+        f32x4 v = eng.acc[i][j];
+        if constexpr (!SPLIT) v += bias[j];
+        return v;
+      });
+      __builtin_amdgcn_sched_barrier(0);   // one row tile's values in registers at a time
+    }
+  }
+};
+
+template <int OUT, bool SAVE>
+struct F8StoreGated {
+  template <class Eng>
+  static constexpr int stores() { return Eng::TM * Eng::TN / 2 * (SAVE ? 3 : 1) * 4 * F8Rows<OUT>::kBytes / 16; }
+  template <class Eng>
+  static __device__ __forceinline__ void run(Eng &eng, const F8Problem &p, const F8Item &t, char *ep) {
+    constexpr int H = Eng::TN / 2;
+    const int inter = p.N >> 1, col0 = t.col_lo + eng.wn * (Eng::WTN / 2), ln = eng.late_lane();
+    const F8Rows<OUT> rows(p.C, t, inter, inter), gu(SAVE ? p.GU : p.C, t, p.N, p.N);
+#pragma unroll
+    for (int i = 0; i < Eng::TM; ++i) {
+      if constexpr (SAVE) {
+        eng.template store_row<H>(gu, ep, ln, i, col0, [&](int j) { return eng.acc[i][j]; });
+        eng.template store_row<H>(gu, ep, ln, i, inter + col0, [&](int j) { return eng.acc[i][H + j]; });
+      }
+      eng.template store_row<H>(rows, ep, ln, i, col0, [&](int j) {
+        f32x4 v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = f8_gate(eng.acc[i][j][x], p.act) * eng.acc[i][H + j][x];
+        return v;
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// The stages are separate LDS objects: with one array and a stage index the
+// compiler's wait-count pass cannot tell a stage being read from one being
+// loaded, and waits for every direct load before each step's first read.
+struct F8Lds {
+  char *s[4];
+  char *ep;      // the epilogue's row buffers
+};
+
+// Wait with vmcnt(A) if `first`, else vmcnt(B), and for LDS.  One block to the
+// compiler: around a branch it would sink the sums' updates past the barrier, which
+// keeps the products they come from in registers.
+template <int A, int B>
+__device__ __forceinline__ void f8_wait_either(bool first) {
+  asm volatile(
+      "s_cmp_lg_u32 %0, 0\n\t"
+      "s_cbranch_scc1 1f\n\t"
+      "s_waitcnt vmcnt(%2)\n"
+      "1:\n\t"
+      "s_waitcnt vmcnt(%1) lgkmcnt(0)"
+      :
+      : "s"(__builtin_amdgcn_readfirstlane(first)), "n"(A < 63 ? A : 63), "n"(B < 63 ? B : 63)
+      : "scc", "memory");
+}
+
+// `work.get(n, item)`: this workgroup's n-th item, false past the last; its
+// fields are uniform over the workgroup.
+template <class Eng, class Store, class Work>
+__device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F8Lds &L) {
+  constexpr int NS = Eng::NS;
+  static_assert(NS >= 2 && NS <= 4, "stages");
+  F8Item ci;
+  if (!work.get(0, ci)) return;
+  Eng eng(p, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
+  eng.prepare(ci);
+  typename Eng::Frags f;
+  auto barrier = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto prologue = [&](auto Ic) {
+    constexpr int I = decltype(Ic)::value;
+    eng.issue(L.s[I], ci, min(ci.s0 + I, ci.s1 - 1));
+  };
+  mx4_unroll(prologue, std::make_integer_sequence<int, NS>{});
+  __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
+  barrier();
+  eng.template head<Eng::start(0)>(L.s[0], f);
+  bool stored = false;   // the last tile's stores may still be in flight
+  for (int n = 1;; ++n) {
+    F8Item ni;
+    const bool more = work.get(n, ni);
+    if (more) eng.prepare(ni);
+    else ni = ci;   // its loads land in stages that no step reads
+    eng.clear();
+    // A wave whose rows all lie past the tile's last multiplies nothing (its
+    // loads and barriers are the workgroup's).
+    const int end = ci.row_lo + eng.wm * Eng::WTM <= ci.row_last ? ci.s1 : ci.s0;
+    // Steps come NS at a time; those past the last load a valid step again and
+    // multiply nothing, which keeps the stages in step with the code.
+    for (int s = ci.s0; s < ci.s1; s += NS) {
+      const bool last = s + NS >= ci.s1, fresh = stored && s == ci.s0;
+      F8Item wi = ci;
+      if (last) wi = ni;
+      const int ws = last ? ni.s0 : s + NS;
+      auto body = [&](auto Ic) {
+        constexpr int I = decltype(Ic)::value;
+        // Wait for this wave's loads of the next step, the oldest but those of
+        // the NS - 2 steps after it (right after a tile also but its stores), meet the
+        // others, all of them done with the stage, and load the step NS ahead into it.
+        auto meet = [&] {
+          constexpr int WAIT = (NS - 2) * Eng::LOADS;
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (I <= NS - 2) f8_wait_either<WAIT + Store::template stores<Eng>(), WAIT>(fresh);
+          else __builtin_amdgcn_s_waitcnt(mx4_wait(WAIT));
+          barrier();
+          eng.issue(L.s[I], wi, min(ws + I, wi.s1 - 1));
+          __builtin_amdgcn_sched_barrier(0);
+        };
+        const char *next = L.s[(I + 1) % NS];
+        if (s + I < end) {
+          eng.template step<Eng::start(I)>(L.s[I], next, f, meet);
+        } else {
+          meet();
+          eng.template head<Eng::start(I + 1)>(next, f);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      mx4_unroll(body, std::make_integer_sequence<int, NS>{});
+    }
+    Store::run(eng, p, ci, L.ep);
+    if (!more) break;
+    ci = ni;
+    stored = true;
+  }
+  // The re-issued loads of the last steps land before the workgroup (and its
+  // LDS) ends.
+  __builtin_amdgcn_s_waitcnt(mx4_wait(0));
+}
+
+// Dense and gated: bands of four row tiles walked column by column, so one weight
+// tile serves the band's row tiles while it is in L2.
+template <class Eng>
+struct F8DenseWork {
+  const F8Problem &p;
+  const int tiles_m, tiles_n;
+  const WorkShare share;
+  __device__ __forceinline__ explicit F8DenseWork(const F8Problem &pr)
+      : p(pr), tiles_m((pr.M + Eng::BM - 1) / Eng::BM),
+        tiles_n(((Eng::GATED ? pr.N >> 1 : pr.N) + Eng::COLS - 1) / Eng::COLS), share(tiles_m * tiles_n * pr.slices) {}
+  __device__ __forceinline__ bool get(int n, F8Item &t) const {
+    int id = share.first + n * share.step;
+    if (id >= share.end) return false;
+    constexpr int G = 4;
+    const int per = tiles_m * tiles_n;
+    t.slice = id / per;
+    id -= t.slice * per;
+    const int band = id / (G * tiles_n), first = band * G, gsz = min(G, tiles_m - first);
+    const int in = id - band * G * tiles_n, tn = in / gsz;
+    t.row_lo = (first + in - tn * gsz) * Eng::BM;
+    t.row_last = min(p.M, t.row_lo + Eng::BM) - 1;
+    t.col_lo = tn * Eng::COLS;
+    t.e = 0;
+    t.s0 = t.slice * p.kseg;
+    t.s1 = min(f8_blocks(p.K), t.s0 + p.kseg);
+    return true;
+  }
+};
+
+// Grouped: the column tiles of an expert's row tile next to each other.  Items
+// come in increasing order, so the wave moves on to the next 64 experts at
+// most E / 64 times.
+template <class Eng>
+struct F8GroupWork {
+  const int tiles_n, steps;
+  RowGroups groups;
+  const WorkShare share;
+  static __device__ __forceinline__ int total(const F8Problem &p) {
+    RowGroups g(p, Eng::BM);
+    while (g.more()) g.next();
+    return g.tiles();
+  }
+  __device__ __forceinline__ explicit F8GroupWork(const F8Problem &p)
+      : tiles_n((p.N + Eng::BN - 1) / Eng::BN), steps(f8_blocks(p.K)), groups(p, Eng::BM), share(total(p) * tiles_n) {}
+  __device__ __forceinline__ bool get(int n, F8Item &t) {
+    const int id = share.first + n * share.step;
+    if (id >= share.end) return false;
+    const int tm = id / tiles_n;
+    int row1;
+    if (!groups.find(tm, t.e, t.row_lo, row1)) return false;
+    t.row_last = row1 - 1;
+    t.col_lo = (id - tm * tiles_n) * Eng::BN;
+    t.slice = t.s0 = 0;
+    t.s1 = steps;
+    return true;
+  }
+};
+
+template <class Eng, class Store, class Work>
+__global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_f8_tiles(F8Problem p) {
+  __shared__ __attribute__((aligned(16))) char s0[Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s1[Eng::STAGE];
+  __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 3 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char ep[Eng::EP];
+  Work work(p);
+  f8_tiles<Eng, Store>(p, work, F8Lds{{s0, s1, s2, s3}, ep});
+}
+
+}  // namespace qg

@@ -58,6 +58,9 @@ enum W8A8Tile { kT256, kT256N, kT128, kT64 };
 // streaming kernel, then tiles of 256 x 256, 128 x 256, 128 x 128, 64 x 128 and
 // 32 x 64.
 enum Mx4Kernel { kMx4Stream, kMx4T256, kMx4T256N, kMx4T128, kMx4T64, kMx4T32 };
+// F8 kernels (f8_gemm.hip), in the order qg_set_override names them: the
+// streaming kernel, then tiles of 256 x 256, 128 x 256, 128 x 128 and 64 x 128.
+enum F8Kernel { kF8Stream, kF8T256, kF8T256N, kF8T128, kF8T64 };
 struct Override {
   int path = kPathAuto;
   int prefill_tile = -1;       // PrefillTile, or -1
@@ -67,6 +70,8 @@ struct Override {
   int w8a8_split = 0;          // W8A8 K slices, or 0
   int mx4_tile = -1;           // Mx4Kernel, or -1
   int mx4_split = 0;           // MX4 K slices, or 0
+  int f8_tile = -1;            // F8Kernel, or -1
+  int f8_split = 0;            // F8 K slices, or 0
 };
 Override dispatch_override();
 
