@@ -50,8 +50,10 @@ struct F8Problem {
 // from col_lo on, of expert e; steps [s0, s1).
 struct F8Item {
   int row_lo, row_last, col_lo, e, slice, s0, s1;
-  const float *scales;    // of the wave's scale load (F8Engine::prepare)
-  uint32_t scale_bytes;
+  // Where the wave's loads start, and how far they may reach (F8Engine::prepare).
+  const uint8_t *a, *b;
+  const float *scales;
+  uint32_t a_bytes, b_bytes, scale_bytes;
 };
 
 template <int BM_, int BN_, int WM_, int WN_, int NS_, bool BROW_, bool GATED_>
@@ -111,12 +113,21 @@ struct F8Engine {
     scale_cut = scale_load() < BM / 64 || BROW ? 0u : 4u;
   }
   __device__ __forceinline__ int scale_load() const { return wave % S_LOADS; }
-  // What a tile's scale loads start from.  (col_lo + r) / 128 = col_lo / 128 + r / 128
-  // for the tile's channels: its columns are a part of 128 or a multiple.
+  // What a tile's loads start from.  A wave's loads bring consecutive rows of A and
+  // consecutive channels of B.  (col_lo + r) / 128 = col_lo / 128 + r / 128 for the
+  // tile's channels: its columns are a part of 128 or a multiple.
   __device__ __forceinline__ void prepare(F8Item &t) const {
+    // Uniform by construction; a division leaves them in vector registers.
+    for (int *x : {&t.row_lo, &t.row_last, &t.col_lo, &t.e, &t.slice, &t.s0, &t.s1}) *x = __builtin_amdgcn_readfirstlane(*x);
+    const int rows = t.row_last - t.row_lo + 1, row = 8 * A_DMA * wave, chan = 8 * B_DMA * wave;
+    const int a_left = rows - row, b_left = GATED ? 8 * B_DMA : p.N - t.col_lo - chan;
+    t.a = p.A + static_cast<size_t>(t.row_lo + row) * p.K;
+    t.a_bytes = a_left > 0 ? static_cast<uint32_t>(min(a_left, 8 * A_DMA)) * static_cast<uint32_t>(p.K) : 0u;
+    t.b = p.B + (static_cast<size_t>(t.e) * p.N + channel(t.col_lo, chan)) * p.K;
+    t.b_bytes = b_left > 0 ? static_cast<uint32_t>(min(b_left, 8 * B_DMA)) * static_cast<uint32_t>(p.K) : 0u;
     if (scale_load() < BM / 64) {
       t.scales = p.SA + t.row_lo;
-      t.scale_bytes = static_cast<uint32_t>(t.row_last - t.row_lo + 1) * 4u;
+      t.scale_bytes = static_cast<uint32_t>(rows) * 4u;
     } else if (BROW) {
       t.scales = p.SB + t.col_lo;
       t.scale_bytes = static_cast<uint32_t>(p.N - t.col_lo) * 4u;
@@ -140,35 +151,26 @@ struct F8Engine {
     }
   }
 
+  // One step's loads: one resource for the wave's rows and one for its channels, the
+  // loads' rows as scalar offsets (which count for its bounds, too).
   __device__ __forceinline__ void issue(char *stage, const F8Item &t, int step) const {
-    const uint32_t K = static_cast<uint32_t>(p.K);
+    const uint32_t k0 = static_cast<uint32_t>(step) * 128u;
     const int rem = p.K - step * 128;   // bytes of the rows left
     uint32_t off[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) off[x] = chunk[x] < rem ? lane_off[x] : kOutside;
-    const int rows = t.row_last - t.row_lo + 1, chans = GATED ? COLS : min(BN, p.N - t.col_lo);
-    // A resource for each load, over the rows from its first on that are left: the
-    // lanes' offsets are the same for all (scalar work instead of registers).
-    auto rsrc = [&](const uint8_t *first, int left) {
-      return __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t *>(first), 0,
-          static_cast<int>(left > 0 ? static_cast<uint32_t>(left) * K - static_cast<uint32_t>(step) * 128u : 0u), kRsrcFlags);
-    };
-    const uint8_t *A = p.A + static_cast<size_t>(t.row_lo) * K + static_cast<size_t>(step) * 128;
+    const auto rA = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(t.a + k0), 0,
+                                                      static_cast<int>(t.a_bytes ? t.a_bytes - k0 : 0u), kRsrcFlags);
+    const auto rB = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(t.b + k0), 0,
+                                                      static_cast<int>(t.b_bytes ? t.b_bytes - k0 : 0u), kRsrcFlags);
 #pragma unroll
-    for (int i = 0; i < A_DMA; ++i) {
-      const int row = wave * A_DMA + i;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(A + static_cast<size_t>(8 * row) * K, rows - 8 * row),
-                                               lds_ptr(stage + row * 1024), 16, static_cast<int>(off[i & 1]), 0, 0, 0);
-    }
-    const uint8_t *B = p.B + static_cast<size_t>(t.e) * p.N * K + static_cast<size_t>(step) * 128;
+    for (int i = 0; i < A_DMA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, lds_ptr(stage + (wave * A_DMA + i) * 1024), 16,
+                                               static_cast<int>(off[i & 1]), 8 * i * p.K, 0, 0);
 #pragma unroll
-    for (int i = 0; i < B_DMA; ++i) {
-      const int row = wave * B_DMA + i;   // gated tiles have all of their channels
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc(B + static_cast<size_t>(channel(t.col_lo, 8 * row)) * K, GATED ? 8 : chans - 8 * row),
-          lds_ptr(stage + STAGE_A + row * 1024), 16, static_cast<int>(off[i & 1]), 0, 0, 0);
-    }
+    for (int i = 0; i < B_DMA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, lds_ptr(stage + STAGE_A + (wave * B_DMA + i) * 1024), 16,
+                                               static_cast<int>(off[i & 1]), 8 * i * p.K, 0, 0);
     const auto rS = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char *>(reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step), 0,
         static_cast<int>(t.scale_bytes - static_cast<uint32_t>(step) * scale_cut), kRsrcFlags);
@@ -240,36 +242,52 @@ struct F8Engine {
   }
   // Which half of f.a step I of the stages starts on.
   static constexpr int start(int I) { return RP % 2 ? I & 1 : 0; }
-  // One step, its first fragments read; `meet` waits for the next stage and gives
-  // this one up.  Two row tiles by one column tile at a time (two matrix instructions),
-  // the sums of the two before applied meanwhile.
-  template <int X0, class Meet>
-  __device__ __forceinline__ void step(const char *stage, const char *next, Frags &f, Meet &&meet) {
+  // A step in two parts: all but the last pair of row tiles, and that pair, with
+  // nothing left to read of the stage, while the next stage's first fragments are
+  // read.  Two row tiles by one column tile at a time (two matrix instructions), the
+  // sums of the two before applied behind them.
+  struct Pending {
     f32x4 t[2][2];
-    float ts[2][2];   // the scales of t's rows
-    [[maybe_unused]] ScalesB sb;
+    float s[2][2];   // the scales of t's rows
+  };
+  __device__ __forceinline__ void product(Pending &d, int g, const Frags &f, int j, int x) {
 #pragma unroll
-    for (int g = 0; g < RP * TN; ++g) {
-      const int rp = g / TN, j = g % TN, x = (X0 + rp) & 1;
-      if (j == 0) {
-        if (rp < RP - 1) {
-          read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
-        } else {
-          meet();
-          read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
-          if constexpr (!BROW) sb = read_sb(next);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        t[g & 1][h] = f8_mfma(f.b[j], f.a[x][h]);
-        ts[g & 1][h] = f.sa[x][h];
-      }
-      if (rp == RP - 1) f.b[j] = read(next, b_addr, j);
-      if (g) apply(t[(g - 1) & 1], (g - 1) / TN, (g - 1) % TN, ts[(g - 1) & 1], f.sb);
-      __builtin_amdgcn_sched_barrier(0);   // one group's results in registers besides the next's
+    for (int h = 0; h < 2; ++h) {
+      d.t[g & 1][h] = f8_mfma(f.b[j], f.a[x][h]);
+      d.s[g & 1][h] = f.sa[x][h];
     }
-    apply(t[(RP * TN - 1) & 1], RP - 1, TN - 1, ts[(RP * TN - 1) & 1], f.sb);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __device__ __forceinline__ void settle(const Pending &d, int g, const ScalesB &sb) {
+    apply(d.t[g & 1], g / TN, g % TN, d.s[g & 1], sb);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <int X0>
+  __device__ __forceinline__ void first(const char *stage, Frags &f) {
+    Pending d;
+#pragma unroll
+    for (int g = 0; g < (RP - 1) * TN; ++g) {
+      const int rp = g / TN, j = g % TN, x = (X0 + rp) & 1;
+      if (j == 0) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
+      product(d, g, f, j, x);
+      if (g) settle(d, g - 1, f.sb);
+    }
+    if constexpr (RP > 1) settle(d, (RP - 1) * TN - 1, f.sb);
+  }
+  template <int X0>
+  __device__ __forceinline__ void second(const char *next, Frags &f) {
+    constexpr int X = (X0 + RP - 1) & 1, G0 = (RP - 1) * TN;
+    Pending d;
+    [[maybe_unused]] ScalesB sb;
+    read_a(next, 0, f.a[X ^ 1], f.sa[X ^ 1]);
+    if constexpr (!BROW) sb = read_sb(next);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      product(d, G0 + j, f, j, X);
+      f.b[j] = read(next, b_addr, j);
+      if (j) settle(d, G0 + j - 1, f.sb);
+    }
+    settle(d, G0 + TN - 1, f.sb);
     // With scales by rows of B (four a column tile) the next step's take the place
     // of this one's, for want of registers.
     if constexpr (BROW) f.sb = read_sb(next);
@@ -404,10 +422,10 @@ struct F8Lds {
 };
 
 // Wait with vmcnt(A) if `first`, else vmcnt(B), and for LDS.  One block to the
-// compiler: around a branch it would sink the sums' updates past the barrier, which
-// keeps the products they come from in registers.
+// compiler, which would sink the sums' updates past a branch and keep the products
+// that they come from in registers.
 template <int A, int B>
-__device__ __forceinline__ void f8_wait_either(bool first) {
+__device__ __forceinline__ void f8_wait_either(int first) {
   asm volatile(
       "s_cmp_lg_u32 %0, 0\n\t"
       "s_cbranch_scc1 1f\n\t"
@@ -443,7 +461,7 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
   barrier();
   eng.template head<Eng::start(0)>(L.s[0], f);
-  bool stored = false;   // the last tile's stores may still be in flight
+  int stored = 0;   // the last tile's stores may still be in flight
   for (int n = 1;; ++n) {
     F8Item ni;
     const bool more = work.get(n, ni);
@@ -456,31 +474,30 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
     // Steps come NS at a time; those past the last load a valid step again and
     // multiply nothing, which keeps the stages in step with the code.
     for (int s = ci.s0; s < ci.s1; s += NS) {
-      const bool last = s + NS >= ci.s1, fresh = stored && s == ci.s0;
+      const bool last = s + NS >= ci.s1;
+      const int fresh = s == ci.s0 ? stored : 0;
       F8Item wi = ci;
       if (last) wi = ni;
       const int ws = last ? ni.s0 : s + NS;
       auto body = [&](auto Ic) {
         constexpr int I = decltype(Ic)::value;
+        const bool live = s + I < end;
+        const char *next = L.s[(I + 1) % NS];
+        if (live) eng.template first<Eng::start(I)>(L.s[I], f);
         // Wait for this wave's loads of the next step, the oldest but those of
         // the NS - 2 steps after it (right after a tile also but its stores), meet the
         // others, all of them done with the stage, and load the step NS ahead into it.
-        auto meet = [&] {
-          constexpr int WAIT = (NS - 2) * Eng::LOADS;
-          __builtin_amdgcn_sched_barrier(0);
-          if constexpr (I <= NS - 2) f8_wait_either<WAIT + Store::template stores<Eng>(), WAIT>(fresh);
-          else __builtin_amdgcn_s_waitcnt(mx4_wait(WAIT));
-          barrier();
-          eng.issue(L.s[I], wi, min(ws + I, wi.s1 - 1));
-          __builtin_amdgcn_sched_barrier(0);
-        };
-        const char *next = L.s[(I + 1) % NS];
-        if (s + I < end) {
-          eng.template step<Eng::start(I)>(L.s[I], next, f, meet);
-        } else {
-          meet();
-          eng.template head<Eng::start(I + 1)>(next, f);
-        }
+        // (No branch around the loads: the compiler would have to assume them missing
+        // and wait for all the others.)
+        constexpr int WAIT = (NS - 2) * Eng::LOADS;
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (I <= NS - 2) f8_wait_either<WAIT + Store::template stores<Eng>(), WAIT>(fresh);
+        else __builtin_amdgcn_s_waitcnt(mx4_wait(WAIT));
+        barrier();
+        eng.issue(L.s[I], wi, min(ws + I, wi.s1 - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        if (live) eng.template second<Eng::start(I)>(next, f);
+        else eng.template head<Eng::start(I + 1)>(next, f);
         __builtin_amdgcn_sched_barrier(0);
       };
       mx4_unroll(body, std::make_integer_sequence<int, NS>{});
@@ -488,7 +505,7 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
     Store::run(eng, p, ci, L.ep);
     if (!more) break;
     ci = ni;
-    stored = true;
+    stored = 1;
   }
   // The re-issued loads of the last steps land before the workgroup (and its
   // LDS) ends.
