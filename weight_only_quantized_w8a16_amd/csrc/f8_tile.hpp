@@ -153,29 +153,46 @@ struct F8Engine {
 
   // One step's loads: one resource for the wave's rows and one for its channels, the
   // loads' rows as scalar offsets (which count for its bounds, too).
-  __device__ __forceinline__ void issue(char *stage, const F8Item &t, int step) const {
+  struct Loads {
+    const void *a, *b, *s;
+    uint32_t a_bytes, b_bytes, s_bytes, off[2];
+    char *stage;
+  };
+  // A step past the tile's last loads that one again, its scales as zeros: it adds
+  // nothing.
+  __device__ __forceinline__ Loads loads(char *stage, const F8Item &t, int step_) const {
+    const int step = min(step_, t.s1 - 1);
     const uint32_t k0 = static_cast<uint32_t>(step) * 128u;
     const int rem = p.K - step * 128;   // bytes of the rows left
-    uint32_t off[2];
+    Loads l;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) off[x] = chunk[x] < rem ? lane_off[x] : kOutside;
-    const auto rA = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(t.a + k0), 0,
-                                                      static_cast<int>(t.a_bytes ? t.a_bytes - k0 : 0u), kRsrcFlags);
-    const auto rB = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(t.b + k0), 0,
-                                                      static_cast<int>(t.b_bytes ? t.b_bytes - k0 : 0u), kRsrcFlags);
+    for (int x = 0; x < 2; ++x) l.off[x] = chunk[x] < rem ? lane_off[x] : kOutside;
+    l.a = t.a + k0;
+    l.b = t.b + k0;
+    l.s = reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step;
+    l.a_bytes = t.a_bytes ? t.a_bytes - k0 : 0u;
+    l.b_bytes = t.b_bytes ? t.b_bytes - k0 : 0u;
+    l.s_bytes = step_ < t.s1 ? t.scale_bytes - static_cast<uint32_t>(step) * scale_cut : 0u;
+    l.stage = stage;
+    return l;
+  }
+  __device__ __forceinline__ void issue(const Loads &l) const {
+    auto rsrc = [](const void *base, uint32_t bytes) {
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kRsrcFlags);
+    };
 #pragma unroll
-    for (int i = 0; i < A_DMA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, lds_ptr(stage + (wave * A_DMA + i) * 1024), 16,
-                                               static_cast<int>(off[i & 1]), 8 * i * p.K, 0, 0);
-#pragma unroll
-    for (int i = 0; i < B_DMA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, lds_ptr(stage + STAGE_A + (wave * B_DMA + i) * 1024), 16,
-                                               static_cast<int>(off[i & 1]), 8 * i * p.K, 0, 0);
-    const auto rS = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step), 0,
-        static_cast<int>(t.scale_bytes - static_cast<uint32_t>(step) * scale_cut), kRsrcFlags);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rS, lds_ptr(stage + STAGE_S + scale_load() * 256), 4,
-                                             static_cast<int>(scale_at), 0, 0, 0);
+    for (int x = 0; x < LOADS; ++x) {
+      const int i = x - A_DMA;
+      if (x < A_DMA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.a, l.a_bytes), lds_ptr(l.stage + (wave * A_DMA + x) * 1024), 16,
+                                                 static_cast<int>(l.off[x & 1]), 8 * x * p.K, 0, 0);
+      else if (i < B_DMA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.b, l.b_bytes), lds_ptr(l.stage + STAGE_A + (wave * B_DMA + i) * 1024), 16,
+                                                 static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.s, l.s_bytes), lds_ptr(l.stage + STAGE_S + scale_load() * 256), 4,
+                                                 static_cast<int>(scale_at), 0, 0, 0);
+    }
   }
 
   // acc[i][j]: lane (nl, q) holds row 16 i + nl, columns 16 j + 4 q .. + 3.
@@ -233,9 +250,8 @@ struct F8Engine {
     }
   }
   // The first fragments of a step.
-  template <int X>
   __device__ __forceinline__ void head(const char *stage, Frags &f) const {
-    read_a(stage, 0, f.a[X], f.sa[X]);
+    read_a(stage, 0, f.a[0], f.sa[0]);
 #pragma unroll
     for (int j = 0; j < TN; ++j) f.b[j] = read(stage, b_addr, j);
     f.sb = read_sb(stage);
@@ -262,28 +278,27 @@ struct F8Engine {
     apply(d.t[g & 1], g / TN, g % TN, d.s[g & 1], sb);
     __builtin_amdgcn_sched_barrier(0);
   }
-  template <int X0>
-  __device__ __forceinline__ void first(const char *stage, Frags &f) {
+  __device__ __forceinline__ void first(const char *stage, Frags &f, int x0) {
     Pending d;
 #pragma unroll
     for (int g = 0; g < (RP - 1) * TN; ++g) {
-      const int rp = g / TN, j = g % TN, x = (X0 + rp) & 1;
+      const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
       if (j == 0) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
       product(d, g, f, j, x);
       if (g) settle(d, g - 1, f.sb);
     }
     if constexpr (RP > 1) settle(d, (RP - 1) * TN - 1, f.sb);
   }
-  template <int X0>
-  __device__ __forceinline__ void second(const char *next, Frags &f) {
-    constexpr int X = (X0 + RP - 1) & 1, G0 = (RP - 1) * TN;
+  __device__ __forceinline__ void second(const char *next, Frags &f, int x0) {
+    constexpr int G0 = (RP - 1) * TN;
+    const int x = (x0 + RP - 1) & 1;
     Pending d;
     [[maybe_unused]] ScalesB sb;
-    read_a(next, 0, f.a[X ^ 1], f.sa[X ^ 1]);
+    read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
     if constexpr (!BROW) sb = read_sb(next);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      product(d, G0 + j, f, j, X);
+      product(d, G0 + j, f, j, x);
       f.b[j] = read(next, b_addr, j);
       if (j) settle(d, G0 + j - 1, f.sb);
     }
@@ -349,7 +364,7 @@ struct F8Rows {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rsrc, offset(r, col), 0, 0);
   }
   __device__ __forceinline__ void put8(int r, int col, u32x4 v) const {
-    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, offset(r, col), 0, kNonTemporal);
+    __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, offset(r, col), 0, 0);
   }
 };
 
@@ -421,22 +436,6 @@ struct F8Lds {
   char *ep;      // the epilogue's row buffers
 };
 
-// Wait with vmcnt(A) if `first`, else vmcnt(B), and for LDS.  One block to the
-// compiler, which would sink the sums' updates past a branch and keep the products
-// that they come from in registers.
-template <int A, int B>
-__device__ __forceinline__ void f8_wait_either(int first) {
-  asm volatile(
-      "s_cmp_lg_u32 %0, 0\n\t"
-      "s_cbranch_scc1 1f\n\t"
-      "s_waitcnt vmcnt(%2)\n"
-      "1:\n\t"
-      "s_waitcnt vmcnt(%1) lgkmcnt(0)"
-      :
-      : "s"(__builtin_amdgcn_readfirstlane(first)), "n"(A < 63 ? A : 63), "n"(B < 63 ? B : 63)
-      : "scc", "memory");
-}
-
 // `work.get(n, item)`: this workgroup's n-th item, false past the last; its
 // fields are uniform over the workgroup.
 template <class Eng, class Store, class Work>
@@ -455,57 +454,58 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   };
   auto prologue = [&](auto Ic) {
     constexpr int I = decltype(Ic)::value;
-    eng.issue(L.s[I], ci, min(ci.s0 + I, ci.s1 - 1));
+    eng.issue(eng.loads(L.s[I], ci, ci.s0 + I));
   };
   mx4_unroll(prologue, std::make_integer_sequence<int, NS>{});
   __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
   barrier();
-  eng.template head<Eng::start(0)>(L.s[0], f);
-  int stored = 0;   // the last tile's stores may still be in flight
-  for (int n = 1;; ++n) {
-    F8Item ni;
-    const bool more = work.get(n, ni);
+  eng.head(L.s[0], f);
+  F8Item ni;
+  bool more;
+  auto look_ahead = [&](int n) {
+    more = work.get(n, ni);
     if (more) eng.prepare(ni);
     else ni = ci;   // its loads land in stages that no step reads
-    eng.clear();
-    // A wave whose rows all lie past the tile's last multiplies nothing (its
-    // loads and barriers are the workgroup's).
-    const int end = ci.row_lo + eng.wm * Eng::WTM <= ci.row_last ? ci.s1 : ci.s0;
-    // Steps come NS at a time; those past the last load a valid step again and
-    // multiply nothing, which keeps the stages in step with the code.
-    for (int s = ci.s0; s < ci.s1; s += NS) {
-      const bool last = s + NS >= ci.s1;
-      const int fresh = s == ci.s0 ? stored : 0;
-      F8Item wi = ci;
-      if (last) wi = ni;
-      const int ws = last ? ni.s0 : s + NS;
-      auto body = [&](auto Ic) {
-        constexpr int I = decltype(Ic)::value;
-        const bool live = s + I < end;
-        const char *next = L.s[(I + 1) % NS];
-        if (live) eng.template first<Eng::start(I)>(L.s[I], f);
-        // Wait for this wave's loads of the next step, the oldest but those of
-        // the NS - 2 steps after it (right after a tile also but its stores), meet the
-        // others, all of them done with the stage, and load the step NS ahead into it.
-        // (No branch around the loads: the compiler would have to assume them missing
-        // and wait for all the others.)
-        constexpr int WAIT = (NS - 2) * Eng::LOADS;
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (I <= NS - 2) f8_wait_either<WAIT + Store::template stores<Eng>(), WAIT>(fresh);
-        else __builtin_amdgcn_s_waitcnt(mx4_wait(WAIT));
-        barrier();
-        eng.issue(L.s[I], wi, min(ws + I, wi.s1 - 1));
-        __builtin_amdgcn_sched_barrier(0);
-        if (live) eng.template second<Eng::start(I)>(next, f);
-        else eng.template head<Eng::start(I + 1)>(next, f);
-        __builtin_amdgcn_sched_barrier(0);
-      };
-      mx4_unroll(body, std::make_integer_sequence<int, NS>{});
-    }
+  };
+  // NS steps from s on; those past the tile's last add nothing, which keeps the
+  // stages in step with the code.  FRESH: the last tile's stores may still be in
+  // flight (a copy of the code of its own, so that the compiler knows how many: else
+  // it waits for all of them).  No branch within: one costs a wave its place in the
+  // queue of the matrix cores, and around a load all that are in flight.
+  auto window = [&](auto Fresh, int s) {
+    constexpr bool FRESH = decltype(Fresh)::value;
+    const bool last = s + NS >= ci.s1;
+    F8Item wi = ci;
+    if (last) wi = ni;
+    const int ws = last ? ni.s0 : s + NS;
+    auto body = [&](auto Ic) {
+      constexpr int I = decltype(Ic)::value;
+      eng.first(L.s[I], f, Eng::start(I));
+      // Wait for this wave's loads of the next step, the oldest but those of
+      // the NS - 2 steps after it (right after a tile also but its stores), meet the
+      // others, all of them done with the stage, and load the step NS ahead into it.
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(
+          mx4_wait((NS - 2) * Eng::LOADS + (FRESH && I <= NS - 2 ? Store::template stores<Eng>() : 0)));
+      barrier();
+      eng.issue(eng.loads(L.s[I], wi, ws + I));
+      __builtin_amdgcn_sched_barrier(0);
+      eng.second(L.s[(I + 1) % NS], f, Eng::start(I));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    mx4_unroll(body, std::make_integer_sequence<int, NS>{});
+  };
+  look_ahead(1);
+  eng.clear();
+  window(std::false_type{}, ci.s0);
+  for (int n = 2;; ++n) {
+    for (int s = ci.s0 + NS; s < ci.s1; s += NS) window(std::false_type{}, s);
     Store::run(eng, p, ci, L.ep);
     if (!more) break;
     ci = ni;
-    stored = 1;
+    look_ahead(n);
+    eng.clear();
+    window(std::true_type{}, ci.s0);
   }
   // The re-issued loads of the last steps land before the workgroup (and its
   // LDS) ends.
