@@ -101,7 +101,7 @@ int qg_version(void);
  *   w8a8_split=<n>                  W8A8 K slices, n >= 1
  *   mx4_tile=auto|stream|T256|T256N|T128|T64|T32   the kernel of the MX4 products
  *   mx4_split=<n>                   MX4 K slices, n >= 1
- *   f8_tile=auto|stream|T256|T256N|T128|T64   the kernel of the F8 products
+ *   f8_tile=auto|stream|T256|T128|T64   the kernel of the F8 products
  *   f8_split=<n>                    F8 K slices, n >= 1
  * Keys not given take their automatic choice; NULL or "" restores every
  * automatic choice.  A forced choice that does not fit a problem (a

@@ -11,7 +11,7 @@ import weight_only_quantized_w8a16_amd as qg
 pytestmark = pytest.mark.gpu
 
 BF, HF, SF = torch.bfloat16, torch.float16, torch.float32
-TILES = ["auto", "stream", "T256", "T256N", "T128", "T64"]
+TILES = ["auto", "stream", "T256", "T128", "T64"]
 
 
 def dev(a):

@@ -212,7 +212,6 @@ hipError_t run_stream(const F8Problem &p, hipStream_t s) {
 // The tiles, in the order qg_set_override names them.
 template <int TILE, bool BROW, bool GATED> struct F8Tiling;
 template <bool BROW, bool GATED> struct F8Tiling<kF8T256, BROW, GATED> { using Eng = F8Engine<256, 256, 2, 4, 2, BROW, GATED>; };
-template <bool BROW, bool GATED> struct F8Tiling<kF8T256N, BROW, GATED> { using Eng = F8Engine<128, 256, 2, 4, 2, BROW, GATED>; };
 template <bool BROW, bool GATED> struct F8Tiling<kF8T128, BROW, GATED> { using Eng = F8Engine<128, 128, 2, 2, 2, BROW, GATED>; };
 template <bool BROW, bool GATED> struct F8Tiling<kF8T64, BROW, GATED> { using Eng = F8Engine<64, 128, 2, 2, 2, BROW, GATED>; };
 
@@ -290,7 +289,6 @@ template <int OUT, int FORM, bool BROW>
 hipError_t run_form(const F8Problem &p, int tile, hipStream_t s) {
   switch (tile) {
     case kF8T256: return run_tiles<OUT, FORM, BROW, kF8T256>(p, s);
-    case kF8T256N: return run_tiles<OUT, FORM, BROW, kF8T256N>(p, s);
     case kF8T128: return run_tiles<OUT, FORM, BROW, kF8T128>(p, s);
     case kF8T64: return run_tiles<OUT, FORM, BROW, kF8T64>(p, s);
     default: return run_stream<OUT, FORM, BROW>(p, s);

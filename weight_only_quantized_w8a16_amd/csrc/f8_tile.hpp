@@ -176,12 +176,13 @@ struct F8Engine {
     l.stage = stage;
     return l;
   }
-  __device__ __forceinline__ void issue(const Loads &l) const {
+  // Loads from .. to - 1 of a step's.
+  __device__ __forceinline__ void issue(const Loads &l, int from, int to) const {
     auto rsrc = [](const void *base, uint32_t bytes) {
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kRsrcFlags);
     };
 #pragma unroll
-    for (int x = 0; x < LOADS; ++x) {
+    for (int x = from; x < to; ++x) {
       const int i = x - A_DMA;
       if (x < A_DMA)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.a, l.a_bytes), lds_ptr(l.stage + (wave * A_DMA + x) * 1024), 16,
@@ -203,12 +204,12 @@ struct F8Engine {
       for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // B's scales of a step: per four columns, or one (gated: two) for the wave.
+  // B's scales of a step by blocks: one (gated: two) for the wave.
   struct ScalesB {
-    std::conditional_t<BROW, f32x4, float> s[BROW ? TN : GATED ? 2 : 1];
+    float s[GATED ? 2 : 1];
   };
   struct Frags {
-    i32x8 a[2][2], b[TN];
+    i32x8 a[2][2], b[BROW ? 2 : TN];
     float sa[2][2];
     ScalesB sb;
   };
@@ -224,89 +225,113 @@ struct F8Engine {
     }
   }
   __device__ __forceinline__ ScalesB read_sb(const char *stage) const {
-    ScalesB s;
     const char *at = stage + STAGE_S + (BM + wn * WTN) * 4;
-    if constexpr (BROW) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) s.s[j] = *reinterpret_cast<const f32x4 *>(at + (16 * j + 4 * q) * 4);
-    } else {
-      s.s[0] = *reinterpret_cast<const float *>(at);
-      if constexpr (GATED) s.s[1] = *reinterpret_cast<const float *>(at + WTN * 2);
-    }
+    ScalesB s;
+    s.s[0] = *reinterpret_cast<const float *>(at);
+    if constexpr (GATED) s.s[1] = *reinterpret_cast<const float *>(at + WTN * 2);
     return s;
+  }
+  // By rows of B: those of a lane's four columns of column tile j.
+  __device__ __forceinline__ f32x4 read_sb(const char *stage, int j) const {
+    return *reinterpret_cast<const f32x4 *>(stage + STAGE_S + (BM + wn * WTN + 16 * j + 4 * q) * 4);
   }
   __device__ __forceinline__ void apply(const f32x4 (&t)[2], int rp, int j, const float (&sa)[2], const ScalesB &sb) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       f32x4 &c = acc[2 * rp + h][j];
-      if constexpr (BROW) {
+      const float s = sa[h] * sb.s[GATED && j >= TN / 2 ? 1 : 0];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) c[v] += t[h][v] * (sa[h] * sb.s[j][v]);
-      } else {
-        const float s = sa[h] * sb.s[GATED && j >= TN / 2 ? 1 : 0];
+      for (int v = 0; v < 4; ++v) c[v] += t[h][v] * s;
+    }
+  }
+  __device__ __forceinline__ void apply(const f32x4 (&t)[2], int rp, int j, const float (&sa)[2], f32x4 sb) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) c[v] += t[h][v] * s;
-      }
+    for (int h = 0; h < 2; ++h) {
+      f32x4 &c = acc[2 * rp + h][j];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) c[v] += t[h][v] * (sa[h] * sb[v]);
     }
   }
   // The first fragments of a step.
   __device__ __forceinline__ void head(const char *stage, Frags &f) const {
     read_a(stage, 0, f.a[0], f.sa[0]);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) f.b[j] = read(stage, b_addr, j);
-    f.sb = read_sb(stage);
+    for (int j = 0; j < (BROW ? 1 : TN); ++j) f.b[j] = read(stage, b_addr, j);
+    if constexpr (!BROW) f.sb = read_sb(stage);
   }
   // Which half of f.a step I of the stages starts on.
   static constexpr int start(int I) { return RP % 2 ? I & 1 : 0; }
-  // A step in two parts: all but the last pair of row tiles, and that pair, with
-  // nothing left to read of the stage, while the next stage's first fragments are
-  // read.  Two row tiles by one column tile at a time (two matrix instructions), the
-  // sums of the two before applied behind them.
+  // A step: two row tiles by one column tile at a time (two matrix instructions), the
+  // sums of the two before applied behind them.  The last pair of row tiles has
+  // nothing left to read of the stage: behind its first product `meet` waits for the
+  // next stage and gives this one up, and its other products run while that stage's
+  // first fragments are read and the step's loads are issued -- behind products,
+  // since the load path takes eight waves' loads one after the other.
   struct Pending {
     f32x4 t[2][2];
     float s[2][2];   // the scales of t's rows
   };
-  __device__ __forceinline__ void product(Pending &d, int g, const Frags &f, int j, int x) {
+  __device__ __forceinline__ void product(Pending &d, int g, const i32x8 &b, const i32x8 (&a)[2], const float (&sa)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      d.t[g & 1][h] = f8_mfma(f.b[j], f.a[x][h]);
-      d.s[g & 1][h] = f.sa[x][h];
+      d.t[g & 1][h] = f8_mfma(b, a[h]);
+      d.s[g & 1][h] = sa[h];
     }
     __builtin_amdgcn_sched_barrier(0);
   }
-  __device__ __forceinline__ void settle(const Pending &d, int g, const ScalesB &sb) {
+  template <class Scales>
+  __device__ __forceinline__ void settle(const Pending &d, int g, const Scales &sb) {
     apply(d.t[g & 1], g / TN, g % TN, d.s[g & 1], sb);
     __builtin_amdgcn_sched_barrier(0);
   }
-  __device__ __forceinline__ void first(const char *stage, Frags &f, int x0) {
+  template <class Meet>
+  __device__ __forceinline__ void step(const char *stage, const char *next, Frags &f, int x0, Meet &&meet) {
     Pending d;
+    Loads l;
+    constexpr int G0 = (RP - 1) * TN, HALF = (LOADS + 1) / 2;
+    // Steps of fewer products than that have no time to lose for their loads.
+    constexpr bool LATE = RP >= 4;
+    if constexpr (BROW) {
+      // With scales by rows of B (four a column tile) there are no registers for all
+      // of B's fragments: they are read again for each pair of row tiles, their
+      // scales with them, and the stage is given up at the step's end.
+      f32x4 sb[2];
 #pragma unroll
-    for (int g = 0; g < (RP - 1) * TN; ++g) {
-      const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
-      if (j == 0) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
-      product(d, g, f, j, x);
-      if (g) settle(d, g - 1, f.sb);
-    }
-    if constexpr (RP > 1) settle(d, (RP - 1) * TN - 1, f.sb);
-  }
-  __device__ __forceinline__ void second(const char *next, Frags &f, int x0) {
-    constexpr int G0 = (RP - 1) * TN;
-    const int x = (x0 + RP - 1) & 1;
-    Pending d;
-    [[maybe_unused]] ScalesB sb;
-    read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
-    if constexpr (!BROW) sb = read_sb(next);
+      for (int g = 0; g < RP * TN; ++g) {
+        const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
+        if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
+        if (g + 1 < RP * TN) f.b[(g + 1) & 1] = read(stage, b_addr, (g + 1) % TN);
+        sb[g & 1] = read_sb(stage, j);
+        product(d, g, f.b[g & 1], f.a[x], f.sa[x]);
+        if (g) settle(d, g - 1, sb[(g - 1) & 1]);
+      }
+      l = meet();
+      issue(l, 0, LOADS);
+      read_a(next, 0, f.a[(x0 + RP) & 1], f.sa[(x0 + RP) & 1]);
+      f.b[0] = read(next, b_addr, 0);
+      settle(d, RP * TN - 1, sb[(RP * TN - 1) & 1]);
+    } else {
+      ScalesB sb;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      product(d, G0 + j, f, j, x);
-      f.b[j] = read(next, b_addr, j);
-      if (j) settle(d, G0 + j - 1, f.sb);
+      for (int g = 0; g < RP * TN; ++g) {
+        const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
+        if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
+        product(d, g, f.b[j], f.a[x], f.sa[x]);
+        if (g) settle(d, g - 1, f.sb);
+        if (g == G0) {
+          l = meet();
+          if (!LATE) issue(l, 0, LOADS);
+          __builtin_amdgcn_sched_barrier(0);
+          read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
+          sb = read_sb(next);
+        }
+        if (rp == RP - 1) f.b[j] = read(next, b_addr, j);
+        if (LATE && g == G0 + 1) issue(l, 0, HALF);
+        if (LATE && g == G0 + TN / 2) issue(l, HALF, LOADS);
+      }
+      settle(d, RP * TN - 1, f.sb);
+      f.sb = sb;
     }
-    settle(d, G0 + TN - 1, f.sb);
-    // With scales by rows of B (four a column tile) the next step's take the place
-    // of this one's, for want of registers.
-    if constexpr (BROW) f.sb = read_sb(next);
-    else f.sb = sb;
   }
 
   // 16-bit results: lane rows q trade with their neighbours across a pair of
@@ -454,7 +479,7 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   };
   auto prologue = [&](auto Ic) {
     constexpr int I = decltype(Ic)::value;
-    eng.issue(eng.loads(L.s[I], ci, ci.s0 + I));
+    eng.issue(eng.loads(L.s[I], ci, ci.s0 + I), 0, Eng::LOADS);
   };
   mx4_unroll(prologue, std::make_integer_sequence<int, NS>{});
   __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
@@ -480,17 +505,16 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
     const int ws = last ? ni.s0 : s + NS;
     auto body = [&](auto Ic) {
       constexpr int I = decltype(Ic)::value;
-      eng.first(L.s[I], f, Eng::start(I));
       // Wait for this wave's loads of the next step, the oldest but those of
       // the NS - 2 steps after it (right after a tile also but its stores), meet the
       // others, all of them done with the stage, and load the step NS ahead into it.
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(
-          mx4_wait((NS - 2) * Eng::LOADS + (FRESH && I <= NS - 2 ? Store::template stores<Eng>() : 0)));
-      barrier();
-      eng.issue(eng.loads(L.s[I], wi, ws + I));
-      __builtin_amdgcn_sched_barrier(0);
-      eng.second(L.s[(I + 1) % NS], f, Eng::start(I));
+      auto meet = [&] {
+        __builtin_amdgcn_s_waitcnt(
+            mx4_wait((NS - 2) * Eng::LOADS + (FRESH && I <= NS - 2 ? Store::template stores<Eng>() : 0)));
+        barrier();
+        return eng.loads(L.s[I], wi, ws + I);
+      };
+      eng.step(L.s[I], L.s[(I + 1) % NS], f, Eng::start(I), meet);
       __builtin_amdgcn_sched_barrier(0);
     };
     mx4_unroll(body, std::make_integer_sequence<int, NS>{});

@@ -87,9 +87,9 @@ bool parse(const char *spec, Override &o) {
     } else if (k == "mx4_split") {
       if (!parse_int(v, 1, 1024, o.mx4_split)) return false;
     } else if (k == "f8_tile") {
-      static const char *names[] = {"stream", "T256", "T256N", "T128", "T64"};
+      static const char *names[] = {"stream", "T256", "T128", "T64"};
       int t = -1;
-      for (int i = 0; i < 5; ++i)
+      for (int i = 0; i < 4; ++i)
         if (v == names[i]) t = i;
       if (t < 0 && v != "auto") return false;
       o.f8_tile = t;

@@ -59,8 +59,8 @@ enum W8A8Tile { kT256, kT256N, kT128, kT64 };
 // 32 x 64.
 enum Mx4Kernel { kMx4Stream, kMx4T256, kMx4T256N, kMx4T128, kMx4T64, kMx4T32 };
 // F8 kernels (f8_gemm.hip), in the order qg_set_override names them: the
-// streaming kernel, then tiles of 256 x 256, 128 x 256, 128 x 128 and 64 x 128.
-enum F8Kernel { kF8Stream, kF8T256, kF8T256N, kF8T128, kF8T64 };
+// streaming kernel, then tiles of 256 x 256, 128 x 128 and 64 x 128.
+enum F8Kernel { kF8Stream, kF8T256, kF8T128, kF8T64 };
 struct Override {
   int path = kPathAuto;
   int prefill_tile = -1;       // PrefillTile, or -1
