@@ -46,7 +46,10 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 // Streaming kernel, for few rows: a workgroup owns 16 rows and NT tiles of 16
 // columns (gated: NT / 2 gate tiles and the up tiles beside them), and its waves
 // take 128-k blocks in turn.  Nothing is shared between waves until their sums
-// meet in LDS.  Bound by HBM.
+// meet in LDS.  Bound by HBM: 1 x 131072 x 2048 (268 MB) 43.5 us, 6.2 TB/s.  Loads of
+// whole 128-byte pieces of eight rows, and a trade between lanes, against 64 bytes
+// of sixteen rows: 50.2 us, and 13 x 18944 x 3584 (68 MB) 16.1 against 19.1 (half
+// pieces ask for every line twice).
 // ---------------------------------------------------------------------------
 template <int NT, bool BROW>
 struct F8StreamBlock {
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int nt = min(nt0 + i % OWN, ctiles - 1) + (i >= OWN ? half : 0);
-    wp[i] = B + static_cast<size_t>(nt * 16 + nl) * K;
+    wp[i] = B + static_cast<size_t>(nt * 16 + (nl & 7)) * K;
     sp[i] = BROW ? SB + nt * 16 + 4 * q : SB + static_cast<size_t>(nt >> 3) * nb;
   }
   const int row = min(row0 + nl, row1 - 1);
@@ -85,13 +88,16 @@ __global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
   const float *sap = p.SA + row;
   using Block = F8StreamBlock<NT, BROW>;
   auto load = [&](int kb, Block &f) {
-    // Chunks past K are read at the row's start and multiplied as zeros.
+    // Chunks past K are read at the row's start and multiplied as zeros.  A load of
+    // the weight takes all 128 bytes of eight rows: lane (nl, q) chunk q + 4 (nl / 8)
+    // of row nl % 8, then of row nl % 8 + 8.
     const size_t k0 = static_cast<size_t>(kb) * 128 + 16 * q, at0 = k0 < static_cast<size_t>(K) ? k0 : 0,
                  at1 = k0 + 64 < static_cast<size_t>(K) ? k0 + 64 : 0;
+    const size_t at = nl < 8 ? at0 : at1;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      f.w[i][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at0));
-      f.w[i][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at1));
+      f.w[i][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at));
+      f.w[i][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(wp[i] + at + 8 * static_cast<size_t>(K)));
       if constexpr (BROW) f.sb[i] = *reinterpret_cast<const f32x4u *>(sp[i] + static_cast<size_t>(kb) * p.N);
       else f.sb[i] = sp[i][kb];
     }
@@ -103,6 +109,16 @@ __global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto mma = [&](int kb, Block &f) {
+    // Lanes nl and nl + 8 trade halves: chunks q and q + 4 of row nl.
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t v0 = f.w[i][0][d], v1 = f.w[i][1][d];
+        const uint32_t got = __builtin_amdgcn_mov_dpp(nl < 8 ? v1 : v0, 0x128, 0xF, 0xF, false);   // row_ror:8
+        f.w[i][0][d] = nl < 8 ? v0 : got;
+        f.w[i][1][d] = nl < 8 ? got : v1;
+      }
     if (kb * 128 + 128 > K) {   // a NaN code past K must not count: zeros on both sides
       const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
@@ -201,12 +217,48 @@ hipError_t run_stream_as(const F8Problem &p, long slabs, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Column tiles a workgroup (NT): a CU reads at most some 24 KB/us whatever its waves
+// ask for, so what counts is that every CU has the same share.  As many column tiles as
+// let every CU have one workgroup, up to six, then half as many (two rounds of
+// workgroups) up to ten, then three.  Measured, NT from 1 on:
+//   tiles / CUs 0.5  (N = 2048, K = 2048, M = 1)   4.0  4.6  5.6  6.4  7.5
+//               1.0  (N = 4096, K = 4096, M = 4)   6.3  7.4  9.1 10.9 13.7
+//               1.25 (N = 5120, K = 5120, M = 8)  11.5  9.4 11.9 14.7 17.5
+//               2.5  (N = 10240, K = 2048, M = 1)  6.8  7.7  6.3  6.9  7.9
+//               3.25 (N = 13312, K = 2048, M = 12) 9.9  8.5 10.4  8.1  9.6
+//               4.6  (N = 18944, K = 3584, M = 13) 19.3 17.9 17.3 19.9 16.1
+//               7.0  (N = 28672, K = 4096, M = 1) 25.2 25.1 26.0 24.1 28.2
+//               32   (N = 131072, K = 2048, M = 1) 47.2 43.5 43.5 44.6 45.1
+// More waves a workgroup (16) and two blocks' loads in flight changed nothing.  Gated
+// workgroups (NT / 2 pairs of tiles) two or four: 13312 x 2048 11.8 and 12.1, 16 x
+// 18944 x 3584 30.6 and 29.8.  A grouped product's workgroups are bounds, most
+// without rows: one, two or four (48 rows over 64 experts of 2816 x 2048 45.6, 35.6
+// and 31.9).
 template <int OUT, int FORM, bool BROW>
 hipError_t run_stream(const F8Problem &p, hipStream_t s) {
   // Row slabs: a grouped product has at most one partial slab per expert
   // with rows.
   const long slabs = FORM == kGrouped ? p.M / 16 + std::min(p.E, p.M) : (static_cast<long>(p.M) + 15) / 16;
-  return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+  const long cus = device_cus(), tiles = FORM == kGated ? p.N >> 5 : p.N >> 4, rounds = (tiles * slabs + cus - 1) / cus;
+  if constexpr (FORM == kGated) {
+    if (rounds <= 4) return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+    return run_stream_as<OUT, 4, FORM, BROW>(p, slabs, s);
+  } else if constexpr (FORM == kGrouped) {
+    if (rounds <= 2) return run_stream_as<OUT, 1, FORM, BROW>(p, slabs, s);
+    if (rounds <= 4) return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+    return run_stream_as<OUT, 4, FORM, BROW>(p, slabs, s);
+  } else if constexpr (BROW) {
+    return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+  } else {
+    switch (rounds <= 6 ? rounds : rounds <= 10 ? (rounds + 1) / 2 : 3) {
+      case 1: return run_stream_as<OUT, 1, FORM, BROW>(p, slabs, s);
+      case 2: return run_stream_as<OUT, 2, FORM, BROW>(p, slabs, s);
+      case 3: return run_stream_as<OUT, 3, FORM, BROW>(p, slabs, s);
+      case 4: return run_stream_as<OUT, 4, FORM, BROW>(p, slabs, s);
+      case 5: return run_stream_as<OUT, 5, FORM, BROW>(p, slabs, s);
+      default: return run_stream_as<OUT, 6, FORM, BROW>(p, slabs, s);
+    }
+  }
 }
 
 // The tiles, in the order qg_set_override names them.
