@@ -19,6 +19,7 @@
 // both operands use the same: lane (nl, q) takes the 16-byte chunks q and q + 4
 // of its row's 128 bytes.
 #include <algorithm>
+#include <cmath>
 
 #include "f8_common.hpp"
 #include "f8_tile.hpp"
@@ -188,9 +189,10 @@ __global__ __launch_bounds__(256) void k_f8_reduce(F8Problem p) {
   const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
   for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4; i < mn; i += step) {
     f32x4 v = *reinterpret_cast<const f32x4 *>(p.part + i);
+#pragma unroll 4
     for (int sl = 1; sl < p.slices; ++sl) v += *reinterpret_cast<const f32x4 *>(p.part + sl * mn + i);
-    const int col = static_cast<int>(i % p.N);
     if (p.bias) {
+      const int col = static_cast<int>(i % p.N);
 #pragma unroll
       for (int x = 0; x < 4; ++x) v[x] += bits_to_f32_dyn(p.bias[col + x], p.bias_dt);
     }
@@ -276,6 +278,44 @@ struct F8Plan {
   size_t bytes;        // partials
 };
 
+// What a tile costs, in microseconds: a launch (t0), per step `full` while a CU
+// runs as many workgroups as it does at a time (most), lone + shared * q with a
+// mean of q < most (lone: a workgroup's chain of steps; shared: what the workgroups
+// take from each other), and `again` for every further round.  Fitted to 1200
+// timings on MI355X, 16 to 4096 rows and 13 weight shapes of 512 x 8192 to 18944 x
+// 3584, dense and gated, each tile and slice count forced, and 90 with B's scales by
+// rows (residual 8 and 6 %); the tile so picked is within 0.4 % of the best one on
+// average, 20 % at worst (100 x 3584 x 3584 in eight slices instead of three).
+struct F8Cost {
+  int tile, bm, bn, most;
+  float t0, lone, shared, full, again;
+};
+constexpr F8Cost kCost[] = {{kF8T256, 256, 256, 1, 6.6f, 1.387f, 0.322f, 1.828f, 1.3f},
+                            {kF8T128, 128, 128, 2, 3.7f, 0.640f, 0.249f, 1.097f, 0.f},
+                            {kF8T64, 64, 128, 2, 2.4f, 0.528f, 0.167f, 0.744f, 0.f}};
+constexpr F8Cost kCostRows[] = {{kF8T256, 256, 256, 1, 7.3f, 1.700f, 0.601f, 2.150f, 4.0f},
+                                {kF8T128, 128, 128, 2, 4.4f, 0.654f, 0.468f, 1.190f, 2.4f},
+                                {kF8T64, 64, 128, 2, 3.7f, 0.510f, 0.120f, 0.682f, 1.6f}};
+// K slices: the reduction's launch, one more slice, and a byte of partials; the
+// streaming kernel's launch, and a byte that a CU reads (all in the same fit).
+constexpr float kSliceLaunch = 2.1f, kSliceEach = 0.24f, kSliceByte = 2.8e-7f;
+constexpr float kStreamLaunch = 3.4f, kStreamByte = 4.44e-5f;
+
+// Time of `tiles` tiles of `steps` steps each.
+float tiles_time(const F8Cost &c, float tiles, int steps) {
+  const float q = tiles / static_cast<float>(device_cus()), most = static_cast<float>(c.most);
+  const float rounds = static_cast<float>(static_cast<int>(q / most)), rest = q - rounds * most;
+  steps += steps & 1;   // two stages
+  return c.t0 + static_cast<float>(steps) * (rounds * c.full + (rest > 0.f ? c.lone + c.shared * rest : 0.f)) +
+         c.again * std::max(0.f, rest > 0.f ? rounds : rounds - 1.f);
+}
+
+// The streaming kernel, or the tile and (dense) the K slices, with the least time by
+// the measured costs.  A grouped product's row tiles are not known to the host: it
+// reckons with half a tile too many for every expert that can have rows, and with a
+// row slab of its own for each in the streaming kernel, which so is taken for few rows
+// on few experts (8 experts, n = 3584, k = 2560: 4 rows 11.6 us against 15.8, 8 rows
+// 17.1 against 16.3; 64 experts, n = 2816, k = 2048: 32 rows 31.4 against 30.8).
 F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
   const int steps = f8_blocks(K);
   F8Plan pl{kF8Stream, steps, 1, 0};
@@ -284,9 +324,39 @@ F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
   // and an expert's scales.
   const uint64_t nb = f8_blocks(N);
   if (uint64_t(256) * 4 * N >= kF8Span || uint64_t(256) * K >= kF8Span || nb * steps * 4 >= kF8Span) return pl;
-  if (ov.f8_tile >= 0) pl.tile = ov.f8_tile;
-  else if (M > 16) pl.tile = M > 1024 ? kF8T256 : M > 128 ? kF8T128 : kF8T64;
-  if (pl.tile == kF8Stream || form != kDense) return pl;
+  if (ov.f8_tile >= 0) {
+    pl.tile = ov.f8_tile;
+  } else {
+    const float experts = static_cast<float>(std::min(E, M));
+    const float slabs = form == kGrouped ? static_cast<float>(M / 16) + experts : static_cast<float>(M / 16 + (M % 16 != 0));
+    const float share = std::ceil(static_cast<float>(N / 16) * slabs / static_cast<float>(device_cus()));
+    float best = kStreamLaunch + kStreamByte * share * 16.f * static_cast<float>(K);
+    for (const F8Cost &c : brow ? kCostRows : kCost) {
+      const int cols = form == kGated ? c.bn / 2 : c.bn, n = form == kGated ? N / 2 : N;
+      const float tiles = static_cast<float>(n / cols + (n % cols != 0)) *
+                          (form == kGrouped ? static_cast<float>(M) / static_cast<float>(c.bm) + 0.5f * experts
+                                            : static_cast<float>(M / c.bm + (M % c.bm != 0)));
+      for (int sl = 1; sl <= 16 && (sl == 1 || (form == kDense && sl <= steps / 2)); ++sl) {
+        const int kseg = (steps + sl - 1) / sl;
+        if ((steps + kseg - 1) / kseg != sl) continue;
+        float t = tiles_time(c, tiles * static_cast<float>(sl), kseg);
+        if (sl > 1)
+          t += kSliceLaunch + static_cast<float>(sl) * kSliceEach +
+               static_cast<float>(sl + 1) * static_cast<float>(M) * static_cast<float>(N) * 4.f * kSliceByte;
+        if (t < best) {
+          best = t;
+          pl.tile = c.tile;
+          pl.slices = sl;
+          pl.kseg = kseg;
+        }
+      }
+    }
+  }
+  if (pl.tile == kF8Stream || form != kDense) {
+    pl.slices = 1;
+    pl.kseg = steps;
+    return pl;
+  }
   if (ov.f8_split > 0) {
     const int want = std::min(ov.f8_split, steps);
     pl.kseg = (steps + want - 1) / want;
