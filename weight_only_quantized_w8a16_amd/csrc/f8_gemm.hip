@@ -300,6 +300,9 @@ constexpr F8Cost kCostRows[] = {{kF8T256, 256, 256, 1, 7.3f, 1.700f, 0.601f, 2.1
 // streaming kernel's launch, and a byte that a CU reads (all in the same fit).
 constexpr float kSliceLaunch = 2.1f, kSliceEach = 0.24f, kSliceByte = 2.8e-7f;
 constexpr float kStreamLaunch = 3.4f, kStreamByte = 4.44e-5f;
+// A byte of weights that the tiles read from memory: what bounds them for few rows of
+// many channels (1 x 131072 x 2048 50 us on 64 x 128 tiles, 43.5 streamed).
+constexpr float kReadByte = 1.8e-7f;
 
 // Time of `tiles` tiles of `steps` steps each.
 float tiles_time(const F8Cost &c, float tiles, int steps) {
@@ -331,6 +334,7 @@ F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
     const float slabs = form == kGrouped ? static_cast<float>(M / 16) + experts : static_cast<float>(M / 16 + (M % 16 != 0));
     const float share = std::ceil(static_cast<float>(N / 16) * slabs / static_cast<float>(device_cus()));
     float best = kStreamLaunch + kStreamByte * share * 16.f * static_cast<float>(K);
+    const float read = kReadByte * static_cast<float>(N) * static_cast<float>(K) * (form == kGrouped ? experts : 1.f);
     for (const F8Cost &c : brow ? kCostRows : kCost) {
       const int cols = form == kGated ? c.bn / 2 : c.bn, n = form == kGated ? N / 2 : N;
       const float tiles = static_cast<float>(n / cols + (n % cols != 0)) *
@@ -339,7 +343,7 @@ F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
       for (int sl = 1; sl <= 16 && (sl == 1 || (form == kDense && sl <= steps / 2)); ++sl) {
         const int kseg = (steps + sl - 1) / sl;
         if ((steps + kseg - 1) / kseg != sl) continue;
-        float t = tiles_time(c, tiles * static_cast<float>(sl), kseg);
+        float t = std::max(tiles_time(c, tiles * static_cast<float>(sl), kseg), c.t0 + read);
         if (sl > 1)
           t += kSliceLaunch + static_cast<float>(sl) * kSliceEach +
                static_cast<float>(sl + 1) * static_cast<float>(M) * static_cast<float>(N) * 4.f * kSliceByte;
