@@ -390,8 +390,9 @@ def quantised_gradient(d, near):
 @pytest.mark.parametrize("m,inter,k", [(1, 128, 16), (16, 128, 272), (35, 256, 144), (130, 384, 272), (300, 128, 528)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("tile", ["auto", "stream", "T256", "T64"])
-def test_gated_backward(m, inter, k, act, dtype, tile):
+@pytest.mark.parametrize("odd_scales", [False, True])
+@pytest.mark.parametrize("tile", ["auto", "stream", "T256", "T128", "T64"])
+def test_gated_backward(m, inter, k, act, dtype, tile, odd_scales):
     qg.set_override(f8_tile=tile)
     rng = np.random.default_rng(m + inter + k)
     x = rng.standard_normal((m, k))
@@ -400,6 +401,9 @@ def test_gated_backward(m, inter, k, act, dtype, tile):
     gu = torch.from_numpy(rng.standard_normal((m, 2 * inter)) * 2).to(dtype)
     *_, xt, xts = qg.quantize_f8(dev(x), transposed=True)
     *_, wt, wts = qg.quantize_f8(dev(w), block=128, transposed=True)
+    if odd_scales:      # one scale of X^T that is no power of two, and none of W's that is
+        xts.view(-1)[xts.numel() // 2] *= 1.25
+        wts *= 1.25
     dx, dw = qg.gated_f8_backward(dh.cuda(), gu.cuda(), xt, xts, wt, wts, act, SF, SF)
 
     g, u, h = gu.double().numpy()[:, :inter], gu.double().numpy()[:, inter:], dh.double().numpy()
@@ -464,6 +468,29 @@ def test_gated_gradients_against_differences(act):
             up = loss(xv + e * v, wv) if point == 0 else loss(xv, wv + e * v)
             down = loss(xv - e * v, wv) if point == 0 else loss(xv, wv - e * v)
             assert abs((up - down) / (2 * e) - (got * v).sum()) <= (bound * np.abs(v)).sum() * 1.01
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -127, 2.0 ** -149, -1.0, 0.0, float("inf"), float("nan"), 2.0 ** -126, 2.0 ** 127])
+@pytest.mark.parametrize("tile", TILES[1:])
+def test_gated_backward_scales_at_the_ends(scale, tile):
+    # scales that a power's exponent field does not stand for, and the last ones it does
+    qg.set_override(f8_tile=tile)
+    m, inter, k = 20, 128, 48
+    dh = torch.ones(m, inter, dtype=BF, device="cuda")
+    gu = torch.zeros(m, 2 * inter, dtype=BF, device="cuda")
+    gu[:, 0] = 2.0                                            # u = 0: only du = act(2)
+    xt, xts = codes8(np.full((k, 32), 0x38, np.uint8)), torch.ones(1, k, device="cuda")   # codes of 1
+    xts[0, 5] = scale
+    _, dw = qg.gated_f8_backward(dh, gu, xt, xts, None, None, dw_dtype=SF)
+    code, row = ref.quantize(np.full((1, 16), ref.gate(np.array(2.0), "silu")[0]))
+    want = np.zeros((2 * inter, k))
+    want[inter] = m * ref.values(code, row)[0, 0]
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):      # the scales' product, rounded to fp32
+        product = np.float64(np.float32(row[0, 0]) * np.float32(scale))
+        want[inter, 5] = m * ref.decode(code)[0, 0] * product
+    if not np.isfinite(scale):                                               # 0 * inf and 0 * NaN are NaN
+        want[:inter, 5] = want[inter + 1:, 5] = np.nan
+    same(dw, want)
 
 
 def test_gated_backward_no_tokens():

@@ -571,14 +571,15 @@ qg_status qgated_f8(const uint8_t *A, const float *AS, const uint8_t *B, const f
 // slices (one product after the other).
 namespace {
 struct GatedWs {
-  size_t d, dt, sd, sdt, part, part_bytes, bytes;
+  size_t d, dt, sd, sdt, powers, part, part_bytes, bytes;
   GatedWs(int m, int inter, int k) {
     const size_t n = 2 * static_cast<size_t>(inter), r = (static_cast<size_t>(m) + 15) / 16 * 16;
     d = 0;
     dt = d + up256(static_cast<size_t>(m) * n);
     sd = dt + up256(n * r);
     sdt = sd + up256(n / 128 * m * sizeof(float));
-    part = sdt + up256((static_cast<size_t>(m) + 127) / 128 * n * sizeof(float));
+    powers = sdt + up256((static_cast<size_t>(m) + 127) / 128 * n * sizeof(float));
+    part = powers + up256(qg::kF8Flags * sizeof(uint32_t));
     const size_t x = qg::f8_workspace_bytes(m, k, 2 * inter, 128),
                  w = qg::f8_workspace_bytes(2 * inter, k, static_cast<int>(r), 1);
     part_bytes = up256(x > w ? x : w);
@@ -615,7 +616,9 @@ qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT, 
   uint8_t *w = static_cast<uint8_t *>(workspace);
   uint8_t *D = dX ? w + ws.d : nullptr, *DT = dW ? w + ws.dt : nullptr;
   float *SD = reinterpret_cast<float *>(w + ws.sd), *SDT = reinterpret_cast<float *>(w + ws.sdt);
-  const qg::F8GatedGrad g{dH, GU, m, inter, static_cast<int>(dt), act, D, SD, DT, SDT};
+  uint32_t *powers = reinterpret_cast<uint32_t *>(w + ws.powers);
+  const qg::F8GatedGrad g{dH, GU, m, inter, static_cast<int>(dt), act, D, SD, DT, SDT, XTS,
+                          (static_cast<size_t>(m) + 127) / 128 * k, powers};
   hipError_t e = qg::launch_gated_f8_grad(g, s);
   if (e != hipSuccess) return mx4_status(e);
   qg::F8Args a{};
@@ -643,6 +646,7 @@ qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT, 
     a.C = dW;
     a.M = 2 * inter;
     a.K = (m + 15) / 16 * 16;
+    a.powers = powers;
     a.out = static_cast<int>(dw_dt);
     if ((e = qg::launch_f8_gemm(a, s)) != hipSuccess) return mx4_status(e);
   }

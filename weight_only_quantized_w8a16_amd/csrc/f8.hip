@@ -166,11 +166,29 @@ __global__ __launch_bounds__(512) void k_f8_tile(const void *X, uint8_t *Q, floa
 }
 
 // D = [dh u act'(g) | dh act(g)] from GU = [g | u], tile (ri, b) of its two halves.
+// Workgroups past the tiles (with columns) look through the other scales of the
+// weight gradient's product: powers[i] = 0 if the i-th of kF8Flags parts holds normal powers
+// of two alone (D's own are).
 template <int DT, bool ROWS, bool COLS>
 __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const void *GU, uint8_t *D, float *SD,
-                                                       uint8_t *DT_, float *SDT, int rows, int inter, int act) {
+                                                       uint8_t *DT_, float *SDT, int rows, int inter, int act,
+                                                       const float *scales, size_t n_scales, uint32_t *powers) {
   __shared__ __attribute__((aligned(16))) F8TileLds L;
   const uint32_t kb = static_cast<uint32_t>(inter) >> 7;
+  if constexpr (COLS) {
+    const uint32_t tiles = kb * f8_blocks(rows);
+    if (blockIdx.x >= tiles) {
+      const uint32_t part = blockIdx.x - tiles;
+      bool bad = false;
+      for (size_t i = part * 512 + threadIdx.x; i < n_scales; i += kF8Flags * 512) bad |= !f8_power(scales[i]);
+      if (__syncthreads_or(bad) == 0) {
+        if (threadIdx.x == 0) powers[part] = 0;
+      } else if (threadIdx.x == 0) {
+        powers[part] = 1;
+      }
+      return;
+    }
+  }
   const uint32_t ri = blockIdx.x / kb, b = blockIdx.x - ri * kb;
   const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
   const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
@@ -293,11 +311,11 @@ hipError_t dequant_as(const uint8_t *Q, const float *S, void *out, int stack, in
 template <int DT>
 hipError_t grad_as(const F8GatedGrad &g, hipStream_t s) {
   const uint64_t tiles = static_cast<uint64_t>(f8_blocks(g.m)) * (g.inter >> 7);
-  if (tiles * 512 > kLaunch) return hipErrorNotSupported;
-  const dim3 grid(static_cast<unsigned>(tiles)), block(512);
+  if ((tiles + kF8Flags) * 512 > kLaunch) return hipErrorNotSupported;
+  const dim3 grid(static_cast<unsigned>(tiles) + (g.DT ? kF8Flags : 0)), block(512);
 #define QG_F8_GRAD(ROWS, COLS)                                                                                   \
   hipLaunchKernelGGL((k_f8_gated_grad<DT, ROWS, COLS>), grid, block, 0, s, g.dH, g.GU, g.D, g.SD, g.DT, g.SDT, g.m, \
-                     g.inter, g.act)
+                     g.inter, g.act, g.scales, g.n_scales, g.powers)
   if (g.D && g.DT) QG_F8_GRAD(true, true);
   else if (g.D) QG_F8_GRAD(true, false);
   else QG_F8_GRAD(false, true);

@@ -31,6 +31,11 @@ struct F8Scale {
     inv = __int_as_float((127 - e) << 23);   // not used where bad
   }
 };
+// Whether a scale is a normal power of two, as the matrix instruction's own are.
+__device__ __forceinline__ bool f8_power(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x807FFFFFu) == 0 && u - 0x800000u < 0x7F000000u;
+}
 __device__ __forceinline__ int f8_top(int top, float v) { return max(top, __float_as_int(v) & 0x7FFFFFFF); }
 
 // Four values of at most 448 in magnitude -> codes, rounded to nearest even.
@@ -68,6 +73,11 @@ __device__ __forceinline__ float f8_gate_slope(float g, int act, float &value) {
 __device__ __forceinline__ f32x4 f8_mfma(i32x8 a, i32x8 b) {
   constexpr int kFP8 = 0;   // operand format code
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, kFP8, kFP8, 0, 0, 0, 0);
+}
+// The same on c, each lane's value of its row scaled by 2^(e - 127), e of 1 .. 254 in
+// the low byte.
+__device__ __forceinline__ f32x4 f8_mfma_powers(i32x8 a, i32x8 b, f32x4 c, uint32_t ea, uint32_t eb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, static_cast<int>(ea), 0, static_cast<int>(eb));
 }
 __device__ __forceinline__ i32x8 f8_frag(u32x4 lo, u32x4 hi) {
   return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),

@@ -264,10 +264,10 @@ hipError_t run_stream(const F8Problem &p, hipStream_t s) {
 }
 
 // The tiles, in the order qg_set_override names them.
-template <int TILE, bool BROW, bool GATED> struct F8Tiling;
-template <bool BROW, bool GATED> struct F8Tiling<kF8T256, BROW, GATED> { using Eng = F8Engine<256, 256, 2, 4, 2, BROW, GATED>; };
-template <bool BROW, bool GATED> struct F8Tiling<kF8T128, BROW, GATED> { using Eng = F8Engine<128, 128, 2, 2, 2, BROW, GATED>; };
-template <bool BROW, bool GATED> struct F8Tiling<kF8T64, BROW, GATED> { using Eng = F8Engine<64, 128, 2, 2, 2, BROW, GATED>; };
+template <int TILE, int KIND, bool GATED> struct F8Tiling;
+template <int KIND, bool GATED> struct F8Tiling<kF8T256, KIND, GATED> { using Eng = F8Engine<256, 256, 2, 4, 2, KIND, GATED>; };
+template <int KIND, bool GATED> struct F8Tiling<kF8T128, KIND, GATED> { using Eng = F8Engine<128, 128, 2, 2, 2, KIND, GATED>; };
+template <int KIND, bool GATED> struct F8Tiling<kF8T64, KIND, GATED> { using Eng = F8Engine<64, 128, 2, 2, 2, KIND, GATED>; };
 
 // 32-bit offsets of the tile kernels stay below this.
 constexpr uint64_t kF8Span = uint64_t(1) << 31;
@@ -396,19 +396,29 @@ hipError_t run_tiles_as(const F8Problem &p, int form, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int OUT, int FORM, bool BROW, int TILE>
-hipError_t run_tiles(const F8Problem &p, hipStream_t s) {
-  using Eng = typename F8Tiling<TILE, BROW, FORM == kGated>::Eng;
+template <int OUT, int FORM, int KIND, int TILE>
+hipError_t run_tiles_of(const F8Problem &p, hipStream_t s) {
+  using Eng = typename F8Tiling<TILE, KIND, FORM == kGated>::Eng;
   if constexpr (FORM == kGated) {
     return p.GU ? run_tiles_as<Eng, F8StoreGated<OUT, true>, F8DenseWork<Eng>>(p, FORM, s)
                 : run_tiles_as<Eng, F8StoreGated<OUT, false>, F8DenseWork<Eng>>(p, FORM, s);
   } else if constexpr (FORM == kGrouped) {
     return run_tiles_as<Eng, F8Store<OUT, false>, F8GroupWork<Eng>>(p, FORM, s);
   } else {
-    if (p.slices == 1) return run_tiles_as<Eng, F8Store<OUT, false>, F8DenseWork<Eng>>(p, FORM, s);
-    const hipError_t e = run_tiles_as<Eng, F8Store<OUT, true>, F8DenseWork<Eng>>(p, FORM, s);
-    return e == hipSuccess ? reduce_f8<OUT>(p, s) : e;
+    return p.slices > 1 ? run_tiles_as<Eng, F8Store<OUT, true>, F8DenseWork<Eng>>(p, FORM, s)
+                        : run_tiles_as<Eng, F8Store<OUT, false>, F8DenseWork<Eng>>(p, FORM, s);
   }
+}
+
+template <int OUT, int FORM, bool BROW, int TILE>
+hipError_t run_tiles(const F8Problem &p, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if constexpr (BROW) {
+    if (p.powers) e = run_tiles_of<OUT, FORM, kByPowers, TILE>(p, s);
+  }
+  if (e == hipSuccess) e = run_tiles_of<OUT, FORM, BROW ? kByRows : kByBlocks, TILE>(p, s);
+  if (e == hipSuccess && p.slices > 1) e = reduce_f8<OUT>(p, s);
+  return e;
 }
 
 template <int OUT, int FORM, bool BROW>
@@ -437,7 +447,7 @@ hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s) {
   const bool brow = a.b_block == 1;
   const F8Plan pl = plan_f8(a.M, a.N, a.K, brow, form, a.E);
   F8Problem p{a.A, a.SA, a.B, a.SB, a.bias, a.C, a.GU, a.M, a.N, a.K, a.bias_dt, a.offsets, a.E, a.act,
-              nullptr, f8_blocks(a.K), 1};
+              nullptr, f8_blocks(a.K), 1, a.powers};
   if (pl.slices > 1 && a.ws && a.ws_bytes >= pl.bytes) {
     p.part = static_cast<float *>(a.ws);
     p.kseg = pl.kseg;

@@ -31,6 +31,9 @@
 namespace qg {
 
 enum { kDense, kGrouped, kGated };   // forms of a product
+// B's scales: by blocks of 128 x 128, by rows, or by rows and, with A's, normal powers
+// of two all of them.
+enum { kByBlocks, kByRows, kByPowers };
 
 struct F8Problem {
   const uint8_t *A;
@@ -44,6 +47,7 @@ struct F8Problem {
   int E, act;
   float *part;            // K slices: fp32 partial sums [slices, M, N], else null
   int kseg, slices;       // steps per slice, slices
+  const uint32_t *powers; // kF8Flags words, 0: all scales are normal powers of two; or null: not known
 };
 
 // One tile: rows [row_lo, row_last] of A and C, channels (gated: gate channels)
@@ -56,10 +60,11 @@ struct F8Item {
   uint32_t a_bytes, b_bytes, scale_bytes;
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int NS_, bool BROW_, bool GATED_>
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int KIND_, bool GATED_>
 struct F8Engine {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
-  static constexpr bool BROW = BROW_, GATED = GATED_;
+  static constexpr int KIND = KIND_;
+  static constexpr bool BROW = KIND != kByBlocks, GATED = GATED_;
   static constexpr int NW = WM * WN, NTHR = 64 * NW;
   static constexpr int WTM = BM / WM, WTN = BN / WN;   // wave tile
   static constexpr int TM = WTM / 16, TN = WTN / 16;   // 16x16 accumulators per wave
@@ -284,13 +289,62 @@ struct F8Engine {
     apply(d.t[g & 1], g / TN, g % TN, d.s[g & 1], sb);
     __builtin_amdgcn_sched_barrier(0);
   }
+  // The products before the last pair of row tiles; a step's loads in two halves,
+  // behind products unless there are too few of them.
+  static constexpr int G0 = (RP - 1) * TN, HALF = (LOADS + 1) / 2;
+  static constexpr bool LATE = RP >= 4;
+
+  // Scales that are powers of two (as the quantizer makes them) ride on the matrix
+  // instruction, which adds to the sums itself: no VALU work.
+  struct Powers {
+    i32x8 a[2][2], b[TN];
+    uint32_t ea[2][2], eb[TN];
+  };
+  __device__ __forceinline__ uint32_t exponent(const char *stage, int slot) const {
+    return *reinterpret_cast<const uint32_t *>(stage + STAGE_S + slot * 4) >> 23;
+  }
+  __device__ __forceinline__ void read_a(const char *stage, int rp, i32x8 (&a)[2], uint32_t (&ea)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[h] = read(stage, a_addr, 2 * rp + h);
+      ea[h] = exponent(stage, wm * WTM + 16 * (2 * rp + h) + nl);
+    }
+  }
+  __device__ __forceinline__ void read_b(const char *stage, int j, i32x8 &b, uint32_t &eb) const {
+    b = read(stage, b_addr, j);
+    eb = exponent(stage, BM + wn * WTN + 16 * j + nl);
+  }
+  __device__ __forceinline__ void head(const char *stage, Powers &f) const {
+    read_a(stage, 0, f.a[0], f.ea[0]);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) read_b(stage, j, f.b[j], f.eb[j]);
+  }
+  template <class Meet>
+  __device__ __forceinline__ void step(const char *stage, const char *next, Powers &f, int x0, Meet &&meet) {
+    Loads l;
+#pragma unroll
+    for (int g = 0; g < RP * TN; ++g) {
+      const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
+      if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.ea[x ^ 1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        acc[2 * rp + h][j] = f8_mfma_powers(f.b[j], f.a[x][h], acc[2 * rp + h][j], f.eb[j], f.ea[x][h]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (g == G0) {
+        l = meet();
+        if (!LATE) issue(l, 0, LOADS);
+        __builtin_amdgcn_sched_barrier(0);
+        read_a(next, 0, f.a[x ^ 1], f.ea[x ^ 1]);
+      }
+      if (rp == RP - 1) read_b(next, j, f.b[j], f.eb[j]);
+      if (LATE && g == G0 + 1) issue(l, 0, HALF);
+      if (LATE && g == G0 + TN / 2) issue(l, HALF, LOADS);
+    }
+  }
   template <class Meet>
   __device__ __forceinline__ void step(const char *stage, const char *next, Frags &f, int x0, Meet &&meet) {
     Pending d;
     Loads l;
-    constexpr int G0 = (RP - 1) * TN, HALF = (LOADS + 1) / 2;
-    // Steps of fewer products than that have no time to lose for their loads.
-    constexpr bool LATE = RP >= 4;
     if constexpr (BROW) {
       // With scales by rows of B (four a column tile) there are no registers for all
       // of B's fragments: they are read again for each pair of row tiles, their
@@ -471,7 +525,6 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   if (!work.get(0, ci)) return;
   Eng eng(p, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
   eng.prepare(ci);
-  typename Eng::Frags f;
   auto barrier = [] {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -484,7 +537,6 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   mx4_unroll(prologue, std::make_integer_sequence<int, NS>{});
   __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
   barrier();
-  eng.head(L.s[0], f);
   F8Item ni;
   bool more;
   auto look_ahead = [&](int n) {
@@ -497,7 +549,7 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   // flight (a copy of the code of its own, so that the compiler knows how many: else
   // it waits for all of them).  No branch within: one costs a wave its place in the
   // queue of the matrix cores, and around a load all that are in flight.
-  auto window = [&](auto Fresh, int s) {
+  auto window = [&](auto Fresh, auto &f, int s) {
     constexpr bool FRESH = decltype(Fresh)::value;
     const bool last = s + NS >= ci.s1;
     F8Item wi = ci;
@@ -520,17 +572,22 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
     mx4_unroll(body, std::make_integer_sequence<int, NS>{});
   };
   look_ahead(1);
-  eng.clear();
-  window(std::false_type{}, ci.s0);
-  for (int n = 2;; ++n) {
-    for (int s = ci.s0 + NS; s < ci.s1; s += NS) window(std::false_type{}, s);
-    Store::run(eng, p, ci, L.ep);
-    if (!more) break;
-    ci = ni;
-    look_ahead(n);
+  auto walk = [&](auto &f) {
+    eng.head(L.s[0], f);
     eng.clear();
-    window(std::true_type{}, ci.s0);
-  }
+    window(std::false_type{}, f, ci.s0);
+    for (int n = 2;; ++n) {
+      for (int s = ci.s0 + NS; s < ci.s1; s += NS) window(std::false_type{}, f, s);
+      Store::run(eng, p, ci, L.ep);
+      if (!more) break;
+      ci = ni;
+      look_ahead(n);
+      eng.clear();
+      window(std::true_type{}, f, ci.s0);
+    }
+  };
+  std::conditional_t<Eng::KIND == kByPowers, typename Eng::Powers, typename Eng::Frags> f;
+  walk(f);
   // The re-issued loads of the last steps land before the workgroup (and its
   // LDS) ends.
   __builtin_amdgcn_s_waitcnt(mx4_wait(0));
@@ -601,6 +658,12 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_f8_tiles(F8Problem p)
   __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? Eng::STAGE : 16];
   __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 3 ? Eng::STAGE : 16];
   __shared__ __attribute__((aligned(16))) char ep[Eng::EP];
+  if constexpr (Eng::BROW) {   // where the scales decide, both kinds are launched, and one has the work
+    if (p.powers) {
+      const bool powers = __ballot(p.powers[threadIdx.x & (kF8Flags - 1)] != 0) == 0;
+      if (powers != (Eng::KIND == kByPowers)) return;
+    }
+  }
   Work work(p);
   f8_tiles<Eng, Store>(p, work, F8Lds{{s0, s1, s2, s3}, ep});
 }

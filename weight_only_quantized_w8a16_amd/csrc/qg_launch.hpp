@@ -252,10 +252,12 @@ struct F8Args {
   void *GU;                 // gated: [M, N] in `out`, or null
   void *ws;                 // K slices' partials, may be null
   size_t ws_bytes;
+  const uint32_t *powers;   // kF8Flags words that are 0 if all scales are normal powers of two, or null
 };
 size_t f8_workspace_bytes(int m, int n, int k, int b_block);
 hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s);
 
+constexpr int kF8Flags = 32;
 // Gradient of H = act(g) * u, quantized by rows (D) and transposed (DT).
 struct F8GatedGrad {
   const void *dH, *GU;      // [m, inter], [m, 2 inter] in dt
@@ -264,6 +266,9 @@ struct F8GatedGrad {
   float *SD;                // [2 inter / 128, m]
   uint8_t *DT;              // [2 inter, m padded to 16], or null
   float *SDT;               // [blocks of m, 2 inter]
+  const float *scales;      // other scales of DT's product, n_scales of them, to look through
+  size_t n_scales;
+  uint32_t *powers;         // kF8Flags words: 0 where all looked at are normal powers of two
 };
 hipError_t launch_gated_f8_grad(const F8GatedGrad &g, hipStream_t s);
 // Zeros (a kernel: it may be captured), a multiple of 16 bytes.
