@@ -470,6 +470,35 @@ def test_gated_gradients_against_differences(act):
             assert abs((up - down) / (2 * e) - (got * v).sum()) <= (bound * np.abs(v)).sum() * 1.01
 
 
+@pytest.mark.parametrize("tile", ["auto", "T256", "T128", "T64"])
+@pytest.mark.parametrize("odd", [False, True])
+def test_gated_backward_large(tile, odd):
+    """Large enough that the scales decide between two kernels for dW; some of its rows against the formula."""
+    m, inter, k = 1030, 2560, 7984
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s, f=1.0: (torch.randn(*s, generator=g, device="cuda") * f).to(BF)   # noqa: E731
+    x, dh, gu = r(m, k), r(m, inter), r(m, 2 * inter)
+    *_, xt, xts = qg.quantize_f8(x, transposed=True)
+    if odd:
+        xts[4, 1000] *= 1.5
+    qg.set_override(f8_tile=tile)
+    _, dw = qg.gated_f8_backward(dh, gu, xt, xts, None, None, dw_dtype=SF)
+    _, again = qg.gated_f8_backward(dh, gu, xt, xts, None, None, dw_dtype=SF)
+    assert torch.equal(dw, again)
+    value, slope = ref.gate(gu[:, :inter].double().cpu().numpy(), "silu")
+    h, u = dh.double().cpu().numpy(), gu[:, inter:].double().cpu().numpy()
+    rows = np.array([0, 1, 127, 128, inter - 1, inter, inter + 77, 2 * inter - 1])
+    d = np.concatenate([h * u * slope, h * value], 1)[:, rows].T
+    y = np.abs(gu[:, :inter].double().cpu().numpy())
+    s = 1 / (1 + np.exp(-gu[:, :inter].double().cpu().numpy()))
+    size = np.concatenate([np.abs(h * u) * (s + y * s * (1 + y)), np.abs(h * value)], 1)[:, rows].T
+    near = (7 * np.concatenate([y, y], 1)[:, rows].T + 16) * 2.0 ** -23 * size
+    dq, off = quantised_gradient(ref.pad16(d), ref.pad16(near))
+    xv = ref.values(bits(xt), host(xts))
+    want = dq @ xv.T
+    close(dw[torch.from_numpy(rows).cuda()], want, sum_bound(dq, xv, dq.shape[1]) + off @ np.abs(xv).T + 2.0 ** -24 * np.abs(want))
+
+
 @pytest.mark.parametrize("scale", [2.0 ** -127, 2.0 ** -149, -1.0, 0.0, float("inf"), float("nan"), 2.0 ** -126, 2.0 ** 127])
 @pytest.mark.parametrize("tile", TILES[1:])
 def test_gated_backward_scales_at_the_ends(scale, tile):

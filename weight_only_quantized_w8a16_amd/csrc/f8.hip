@@ -100,8 +100,10 @@ __device__ __forceinline__ void f8_emit(const float (&v)[4][8], F8TileLds &L, co
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       int m = f8_top(f8_top(f8_top(f8_top(0, v[0][e]), v[1][e]), v[2][e]), v[3][e]);
-      m = max(m, __shfl_xor(m, 16));
-      m = max(m, __shfl_xor(m, 32));
+      const auto half = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+      m = max(static_cast<int>(half[0]), static_cast<int>(half[1]));
+      const auto row = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+      m = max(static_cast<int>(row[0]), static_cast<int>(row[1]));
       if ((t & 63) < 16) atomicMax(&L.top[c + e], m);
     }
     __syncthreads();
@@ -172,11 +174,12 @@ __global__ __launch_bounds__(512) void k_f8_tile(const void *X, uint8_t *Q, floa
 template <int DT, bool ROWS, bool COLS>
 __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const void *GU, uint8_t *D, float *SD,
                                                        uint8_t *DT_, float *SDT, int rows, int inter, int act,
-                                                       const float *scales, size_t n_scales, uint32_t *powers) {
+                                                       const float *scales, size_t n_scales, uint32_t *powers,
+                                                       int halves) {
   __shared__ __attribute__((aligned(16))) F8TileLds L;
   const uint32_t kb = static_cast<uint32_t>(inter) >> 7;
   if constexpr (COLS) {
-    const uint32_t tiles = kb * f8_blocks(rows);
+    const uint32_t tiles = kb * f8_blocks(rows) * halves;
     if (blockIdx.x >= tiles) {
       const uint32_t part = blockIdx.x - tiles;
       bool bad = false;
@@ -189,7 +192,9 @@ __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const voi
       return;
     }
   }
-  const uint32_t ri = blockIdx.x / kb, b = blockIdx.x - ri * kb;
+  // halves 2: a workgroup for each half, where there are few.
+  const uint32_t tile = blockIdx.x / halves, ri = tile / kb, b = tile - ri * kb;
+  const int first = halves == 2 ? static_cast<int>(blockIdx.x & 1) : 0, last = halves == 2 ? first : 1;
   const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
   const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
   const size_t wide = 2 * static_cast<size_t>(inter), pad = f8_pad16(rows);
@@ -213,11 +218,12 @@ __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const voi
   }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    if (half < first || half > last) continue;
     const int n0 = col0 + half * inter;
     const F8TileOut o{D, ROWS ? SD + static_cast<size_t>(n0 >> 7) * rows + row0 : nullptr, DT_,
                       COLS ? SDT + static_cast<size_t>(ri) * wide + n0 : nullptr, wide, pad};
     if (half) {
-      __syncthreads();
+      if (first == 0) __syncthreads();
       f8_emit<false, ROWS, COLS>(du, L, o, row0, rows, n0, 2 * inter);
     } else {
       f8_emit<false, ROWS, COLS>(dg, L, o, row0, rows, n0, 2 * inter);
@@ -310,12 +316,14 @@ hipError_t dequant_as(const uint8_t *Q, const float *S, void *out, int stack, in
 
 template <int DT>
 hipError_t grad_as(const F8GatedGrad &g, hipStream_t s) {
-  const uint64_t tiles = static_cast<uint64_t>(f8_blocks(g.m)) * (g.inter >> 7);
+  uint64_t tiles = static_cast<uint64_t>(f8_blocks(g.m)) * (g.inter >> 7);
+  const int halves = tiles <= static_cast<uint64_t>(device_cus()) ? 2 : 1;
+  tiles *= halves;
   if ((tiles + kF8Flags) * 512 > kLaunch) return hipErrorNotSupported;
   const dim3 grid(static_cast<unsigned>(tiles) + (g.DT ? kF8Flags : 0)), block(512);
 #define QG_F8_GRAD(ROWS, COLS)                                                                                   \
   hipLaunchKernelGGL((k_f8_gated_grad<DT, ROWS, COLS>), grid, block, 0, s, g.dH, g.GU, g.D, g.SD, g.DT, g.SDT, g.m, \
-                     g.inter, g.act, g.scales, g.n_scales, g.powers)
+                     g.inter, g.act, g.scales, g.n_scales, g.powers, halves)
   if (g.D && g.DT) QG_F8_GRAD(true, true);
   else if (g.D) QG_F8_GRAD(true, false);
   else QG_F8_GRAD(false, true);
