@@ -290,7 +290,7 @@ struct F8Cost {
   int tile, bm, bn, most;
   float t0, lone, shared, full, again;
 };
-constexpr F8Cost kCost[] = {{kF8T256, 256, 256, 1, 6.6f, 1.387f, 0.322f, 1.828f, 1.3f},
+constexpr F8Cost kCost[] = {{kF8T256, 256, 256, 1, 6.6f, 1.332f, 0.309f, 1.755f, 1.3f},
                             {kF8T128, 128, 128, 2, 3.7f, 0.640f, 0.249f, 1.097f, 0.f},
                             {kF8T64, 64, 128, 2, 2.4f, 0.528f, 0.167f, 0.744f, 0.f}};
 constexpr F8Cost kCostRows[] = {{kF8T256, 256, 256, 1, 7.3f, 1.700f, 0.601f, 2.150f, 4.0f},

@@ -6,9 +6,20 @@
 // Per step the operands' bytes and scales go from global memory straight into
 // one of NS LDS stages (buffer_load ... lds), NS steps ahead of use and across
 // tile borders.  Each wave waits for its own loads of the next step and meets
-// the others at one barrier a step, when three quarters (or all but two row tiles)
-// of the step are multiplied and all of it is in registers.  What is left
-// multiplies while the next step's first fragments are read.
+// the others at one barrier a step, in front of the products of its last pair of row
+// tiles, when all of the step is in registers.  What is left multiplies while the
+// next step's first fragments are read.  Tiles of four such pairs meet once more,
+// behind the first: B's fragments are in registers then, and its half of the stage is
+// loaded a step's half earlier, so that the loads of a step do not come all at once
+// (4096 x 18944 x 3584 275 -> 266 us, 4096 x 3584 x 37888 516 -> 485, 8192^3 477 -> 457,
+// gated 4096 x 18944 x 3584 with both sums stored 597 -> 565).
+//
+// What bounds the large tile: 8192^3 runs at 2.4 PF of the 4.2 that the matrix
+// instruction reaches alone (2.07 GHz under this load).  No unit is full by the counters:
+// the matrix unit is 53% busy, LDS reads take a quarter of their rate, the L2 is missed
+// only by what the tiles' sharing cannot spare, and a step with the scales on the matrix instruction
+// (no VALU work) takes as long as one without.  What remains is waiting: two waves a
+// SIMD, all that the accumulators leave room for, that meet twice a step.
 //
 // A stage holds BM rows of A and BN rows of B, 128 bytes each, 16-byte chunk c
 // of row r at chunk c ^ ((r / 2) % 8): 16 lanes reading one chunk of 16 rows touch 16
@@ -50,6 +61,11 @@ struct F8Problem {
   const uint32_t *powers; // kF8Flags words, 0: all scales are normal powers of two; or null: not known
 };
 
+// A stage: A's rows and the scales, and B's rows.
+struct F8Stage {
+  char *a, *b;
+};
+
 // One tile: rows [row_lo, row_last] of A and C, channels (gated: gate channels)
 // from col_lo on, of expert e; steps [s0, s1).
 struct F8Item {
@@ -72,7 +88,7 @@ struct F8Engine {
   static constexpr int COLS = GATED ? BN / 2 : BN;     // columns of C a tile
   static constexpr int A_DMA = BM / 8 / NW, B_DMA = BN / 8 / NW;   // 1 KiB loads (8 rows) a wave and step
   static constexpr int S_LOADS = (BM + BN) / 64;       // 64 scales, a load a wave
-  static constexpr int STAGE_A = BM * 128, STAGE_S = STAGE_A + BN * 128, STAGE = STAGE_S + (BM + BN) * 4;
+  static constexpr int STAGE_S = BM * 128, STAGE_A = STAGE_S + (BM + BN) * 4, STAGE_B = BN * 128, STAGE = STAGE_A + STAGE_B;
   static constexpr int LOADS = A_DMA + B_DMA + 1;
   static constexpr int WAVES = 2;   // a SIMD
   static constexpr int EP_ROWS = 16, EP = NW * EP_ROWS * WTN * 2;
@@ -98,7 +114,7 @@ struct F8Engine {
       chunk[x] = ((lane & 7) ^ ((4 * x + (lane >> 4)) & 7)) << 4;
       lane_off[x] = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.K) + chunk[x];
       a_addr[x] = (wm * WTM + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
-      b_addr[x] = STAGE_A + (wn * WTN + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
+      b_addr[x] = (wn * WTN + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
     }
     // 64 scales a wave and step: of 64 rows of A or, behind them, channels of B.
     // With fewer such loads than waves, waves repeat one (the same values to the
@@ -161,11 +177,11 @@ struct F8Engine {
   struct Loads {
     const void *a, *b, *s;
     uint32_t a_bytes, b_bytes, s_bytes, off[2];
-    char *stage;
+    F8Stage stage;
   };
   // A step past the tile's last loads that one again, its scales as zeros: it adds
   // nothing.
-  __device__ __forceinline__ Loads loads(char *stage, const F8Item &t, int step_) const {
+  __device__ __forceinline__ Loads loads(const F8Stage &stage, const F8Item &t, int step_) const {
     const int step = min(step_, t.s1 - 1);
     const uint32_t k0 = static_cast<uint32_t>(step) * 128u;
     const int rem = p.K - step * 128;   // bytes of the rows left
@@ -181,24 +197,29 @@ struct F8Engine {
     l.stage = stage;
     return l;
   }
-  // Loads from .. to - 1 of a step's.
-  __device__ __forceinline__ void issue(const Loads &l, int from, int to) const {
-    auto rsrc = [](const void *base, uint32_t bytes) {
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kRsrcFlags);
-    };
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kRsrcFlags);
+  }
+  __device__ __forceinline__ void issue_a(const Loads &l, int from, int to) const {
 #pragma unroll
-    for (int x = from; x < to; ++x) {
-      const int i = x - A_DMA;
-      if (x < A_DMA)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.a, l.a_bytes), lds_ptr(l.stage + (wave * A_DMA + x) * 1024), 16,
-                                                 static_cast<int>(l.off[x & 1]), 8 * x * p.K, 0, 0);
-      else if (i < B_DMA)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.b, l.b_bytes), lds_ptr(l.stage + STAGE_A + (wave * B_DMA + i) * 1024), 16,
-                                                 static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.s, l.s_bytes), lds_ptr(l.stage + STAGE_S + scale_load() * 256), 4,
-                                                 static_cast<int>(scale_at), 0, 0, 0);
-    }
+    for (int i = from; i < to; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.a, l.a_bytes), lds_ptr(l.stage.a + (wave * A_DMA + i) * 1024), 16,
+                                               static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
+  }
+  __device__ __forceinline__ void issue_scales(const Loads &l) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.s, l.s_bytes), lds_ptr(l.stage.a + STAGE_S + scale_load() * 256), 4,
+                                             static_cast<int>(scale_at), 0, 0, 0);
+  }
+  __device__ __forceinline__ void issue_b(const Loads &l) const {
+#pragma unroll
+    for (int i = 0; i < B_DMA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.b, l.b_bytes), lds_ptr(l.stage.b + (wave * B_DMA + i) * 1024), 16,
+                                               static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
+  }
+  __device__ __forceinline__ void issue(const Loads &l) const {
+    issue_b(l);
+    issue_a(l, 0, A_DMA);
+    issue_scales(l);
   }
 
   // acc[i][j]: lane (nl, q) holds row 16 i + nl, columns 16 j + 4 q .. + 3.
@@ -222,23 +243,23 @@ struct F8Engine {
     return f8_frag(*reinterpret_cast<const u32x4 *>(stage + addr[0] + 2048 * i),
                    *reinterpret_cast<const u32x4 *>(stage + addr[1] + 2048 * i));
   }
-  __device__ __forceinline__ void read_a(const char *stage, int rp, i32x8 (&a)[2], float (&sa)[2]) const {
+  __device__ __forceinline__ void read_a(const F8Stage &stage, int rp, i32x8 (&a)[2], float (&sa)[2]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      a[h] = read(stage, a_addr, 2 * rp + h);
-      sa[h] = *reinterpret_cast<const float *>(stage + STAGE_S + (wm * WTM + 16 * (2 * rp + h) + nl) * 4);
+      a[h] = read(stage.a, a_addr, 2 * rp + h);
+      sa[h] = *reinterpret_cast<const float *>(stage.a + STAGE_S + (wm * WTM + 16 * (2 * rp + h) + nl) * 4);
     }
   }
-  __device__ __forceinline__ ScalesB read_sb(const char *stage) const {
-    const char *at = stage + STAGE_S + (BM + wn * WTN) * 4;
+  __device__ __forceinline__ ScalesB read_sb(const F8Stage &stage) const {
+    const char *at = stage.a + STAGE_S + (BM + wn * WTN) * 4;
     ScalesB s;
     s.s[0] = *reinterpret_cast<const float *>(at);
     if constexpr (GATED) s.s[1] = *reinterpret_cast<const float *>(at + WTN * 2);
     return s;
   }
   // By rows of B: those of a lane's four columns of column tile j.
-  __device__ __forceinline__ f32x4 read_sb(const char *stage, int j) const {
-    return *reinterpret_cast<const f32x4 *>(stage + STAGE_S + (BM + wn * WTN + 16 * j + 4 * q) * 4);
+  __device__ __forceinline__ f32x4 read_sb(const F8Stage &stage, int j) const {
+    return *reinterpret_cast<const f32x4 *>(stage.a + STAGE_S + (BM + wn * WTN + 16 * j + 4 * q) * 4);
   }
   __device__ __forceinline__ void apply(const f32x4 (&t)[2], int rp, int j, const float (&sa)[2], const ScalesB &sb) {
 #pragma unroll
@@ -258,10 +279,10 @@ struct F8Engine {
     }
   }
   // The first fragments of a step.
-  __device__ __forceinline__ void head(const char *stage, Frags &f) const {
+  __device__ __forceinline__ void head(const F8Stage &stage, Frags &f) const {
     read_a(stage, 0, f.a[0], f.sa[0]);
 #pragma unroll
-    for (int j = 0; j < (BROW ? 1 : TN); ++j) f.b[j] = read(stage, b_addr, j);
+    for (int j = 0; j < (BROW ? 1 : TN); ++j) f.b[j] = read(stage.b, b_addr, j);
     if constexpr (!BROW) f.sb = read_sb(stage);
   }
   // Which half of f.a step I of the stages starts on.
@@ -289,10 +310,13 @@ struct F8Engine {
     apply(d.t[g & 1], g / TN, g % TN, d.s[g & 1], sb);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // The products before the last pair of row tiles; a step's loads in two halves,
-  // behind products unless there are too few of them.
-  static constexpr int G0 = (RP - 1) * TN, HALF = (LOADS + 1) / 2;
-  static constexpr bool LATE = RP >= 4;
+  // The products before the last pair of row tiles.  With four pairs a step's loads
+  // are spread: all waves have B's fragments in registers behind the first pair,
+  // so there they meet once more, and that part of the stage is loaded early; A's
+  // loads come one behind a product.  Steps of fewer products load all at once.
+  static constexpr int G0 = (RP - 1) * TN;
+  static constexpr bool EARLY = RP >= 4 && KIND != kByRows;
+  static constexpr int LATER = EARLY ? B_DMA : 0;   // loads in flight at `meet` that belong to a later step
 
   // Scales that are powers of two (as the quantizer makes them) ride on the matrix
   // instruction, which adds to the sums itself: no VALU work.
@@ -300,51 +324,63 @@ struct F8Engine {
     i32x8 a[2][2], b[TN];
     uint32_t ea[2][2], eb[TN];
   };
-  __device__ __forceinline__ uint32_t exponent(const char *stage, int slot) const {
-    return *reinterpret_cast<const uint32_t *>(stage + STAGE_S + slot * 4) >> 23;
+  __device__ __forceinline__ uint32_t exponent(const F8Stage &stage, int slot) const {
+    return *reinterpret_cast<const uint32_t *>(stage.a + STAGE_S + slot * 4) >> 23;
   }
-  __device__ __forceinline__ void read_a(const char *stage, int rp, i32x8 (&a)[2], uint32_t (&ea)[2]) const {
+  __device__ __forceinline__ void read_a(const F8Stage &stage, int rp, i32x8 (&a)[2], uint32_t (&ea)[2]) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      a[h] = read(stage, a_addr, 2 * rp + h);
+      a[h] = read(stage.a, a_addr, 2 * rp + h);
       ea[h] = exponent(stage, wm * WTM + 16 * (2 * rp + h) + nl);
     }
   }
-  __device__ __forceinline__ void read_b(const char *stage, int j, i32x8 &b, uint32_t &eb) const {
-    b = read(stage, b_addr, j);
+  __device__ __forceinline__ void read_b(const F8Stage &stage, int j, i32x8 &b, uint32_t &eb) const {
+    b = read(stage.b, b_addr, j);
     eb = exponent(stage, BM + wn * WTN + 16 * j + nl);
   }
-  __device__ __forceinline__ void head(const char *stage, Powers &f) const {
+  __device__ __forceinline__ void head(const F8Stage &stage, Powers &f) const {
     read_a(stage, 0, f.a[0], f.ea[0]);
 #pragma unroll
     for (int j = 0; j < TN; ++j) read_b(stage, j, f.b[j], f.eb[j]);
   }
-  template <class Meet>
-  __device__ __forceinline__ void step(const char *stage, const char *next, Powers &f, int x0, Meet &&meet) {
-    Loads l;
+  // The loads of a step (l) around its products: behind product g of it.
+  __device__ __forceinline__ void load_behind(const Loads &l, int g) const {
+    if (!EARLY) return;
+    if (g == TN) issue_b(l);
+    if (g == G0 + 1) {
+      issue_a(l, 0, A_DMA / 2);
+      issue_scales(l);
+    }
+    if (g == G0 + TN / 2) issue_a(l, A_DMA / 2, A_DMA);
+  }
+  // `l`: the loads of the step NS ahead; `together`: a barrier; `meet`: the wait for
+  // the next stage and a barrier.
+  template <class Together, class Meet>
+  __device__ __forceinline__ void step(const F8Stage &stage, const F8Stage &next, Powers &f, int x0, const Loads &l,
+                                       Together &&together, Meet &&meet) {
 #pragma unroll
     for (int g = 0; g < RP * TN; ++g) {
       const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
+      if (EARLY && g == TN) together();
       if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.ea[x ^ 1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         acc[2 * rp + h][j] = f8_mfma_powers(f.b[j], f.a[x][h], acc[2 * rp + h][j], f.eb[j], f.ea[x][h]);
       __builtin_amdgcn_sched_barrier(0);
       if (g == G0) {
-        l = meet();
-        if (!LATE) issue(l, 0, LOADS);
+        meet();
+        if (!EARLY) issue(l);
         __builtin_amdgcn_sched_barrier(0);
         read_a(next, 0, f.a[x ^ 1], f.ea[x ^ 1]);
       }
       if (rp == RP - 1) read_b(next, j, f.b[j], f.eb[j]);
-      if (LATE && g == G0 + 1) issue(l, 0, HALF);
-      if (LATE && g == G0 + TN / 2) issue(l, HALF, LOADS);
+      load_behind(l, g);
     }
   }
-  template <class Meet>
-  __device__ __forceinline__ void step(const char *stage, const char *next, Frags &f, int x0, Meet &&meet) {
+  template <class Together, class Meet>
+  __device__ __forceinline__ void step(const F8Stage &stage, const F8Stage &next, Frags &f, int x0, const Loads &l,
+                                       Together &&together, Meet &&meet) {
     Pending d;
-    Loads l;
     if constexpr (BROW) {
       // With scales by rows of B (four a column tile) there are no registers for all
       // of B's fragments: they are read again for each pair of row tiles, their
@@ -354,34 +390,34 @@ struct F8Engine {
       for (int g = 0; g < RP * TN; ++g) {
         const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
         if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
-        if (g + 1 < RP * TN) f.b[(g + 1) & 1] = read(stage, b_addr, (g + 1) % TN);
+        if (g + 1 < RP * TN) f.b[(g + 1) & 1] = read(stage.b, b_addr, (g + 1) % TN);
         sb[g & 1] = read_sb(stage, j);
         product(d, g, f.b[g & 1], f.a[x], f.sa[x]);
         if (g) settle(d, g - 1, sb[(g - 1) & 1]);
       }
-      l = meet();
-      issue(l, 0, LOADS);
+      meet();
+      issue(l);
       read_a(next, 0, f.a[(x0 + RP) & 1], f.sa[(x0 + RP) & 1]);
-      f.b[0] = read(next, b_addr, 0);
+      f.b[0] = read(next.b, b_addr, 0);
       settle(d, RP * TN - 1, sb[(RP * TN - 1) & 1]);
     } else {
       ScalesB sb;
 #pragma unroll
       for (int g = 0; g < RP * TN; ++g) {
         const int rp = g / TN, j = g % TN, x = (x0 + rp) & 1;
+        if (EARLY && g == TN) together();
         if (j == 0 && rp < RP - 1) read_a(stage, rp + 1, f.a[x ^ 1], f.sa[x ^ 1]);
         product(d, g, f.b[j], f.a[x], f.sa[x]);
         if (g) settle(d, g - 1, f.sb);
         if (g == G0) {
-          l = meet();
-          if (!LATE) issue(l, 0, LOADS);
+          meet();
+          if (!EARLY) issue(l);
           __builtin_amdgcn_sched_barrier(0);
           read_a(next, 0, f.a[x ^ 1], f.sa[x ^ 1]);
           sb = read_sb(next);
         }
-        if (rp == RP - 1) f.b[j] = read(next, b_addr, j);
-        if (LATE && g == G0 + 1) issue(l, 0, HALF);
-        if (LATE && g == G0 + TN / 2) issue(l, HALF, LOADS);
+        if (rp == RP - 1) f.b[j] = read(next.b, b_addr, j);
+        load_behind(l, g);
       }
       settle(d, RP * TN - 1, f.sb);
       f.sb = sb;
@@ -507,11 +543,11 @@ struct F8StoreGated {
   }
 };
 
-// The stages are separate LDS objects: with one array and a stage index the
+// The stages, and their halves, are separate LDS objects: with one array and an index the
 // compiler's wait-count pass cannot tell a stage being read from one being
 // loaded, and waits for every direct load before each step's first read.
 struct F8Lds {
-  char *s[4];
+  F8Stage s[2];
   char *ep;      // the epilogue's row buffers
 };
 
@@ -520,7 +556,7 @@ struct F8Lds {
 template <class Eng, class Store, class Work>
 __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F8Lds &L) {
   constexpr int NS = Eng::NS;
-  static_assert(NS >= 2 && NS <= 4, "stages");
+  static_assert(NS == 2, "stages");
   F8Item ci;
   if (!work.get(0, ci)) return;
   Eng eng(p, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
@@ -532,7 +568,7 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
   };
   auto prologue = [&](auto Ic) {
     constexpr int I = decltype(Ic)::value;
-    eng.issue(eng.loads(L.s[I], ci, ci.s0 + I), 0, Eng::LOADS);
+    eng.issue(eng.loads(L.s[I], ci, ci.s0 + I));
   };
   mx4_unroll(prologue, std::make_integer_sequence<int, NS>{});
   __builtin_amdgcn_s_waitcnt(mx4_wait((NS - 1) * Eng::LOADS));
@@ -562,11 +598,10 @@ __device__ __forceinline__ void f8_tiles(const F8Problem &p, Work &work, const F
       // others, all of them done with the stage, and load the step NS ahead into it.
       auto meet = [&] {
         __builtin_amdgcn_s_waitcnt(
-            mx4_wait((NS - 2) * Eng::LOADS + (FRESH && I <= NS - 2 ? Store::template stores<Eng>() : 0)));
+            mx4_wait((NS - 2) * Eng::LOADS + Eng::LATER + (FRESH && I <= NS - 2 ? Store::template stores<Eng>() : 0)));
         barrier();
-        return eng.loads(L.s[I], wi, ws + I);
       };
-      eng.step(L.s[I], L.s[(I + 1) % NS], f, Eng::start(I), meet);
+      eng.step(L.s[I], L.s[(I + 1) % NS], f, Eng::start(I), eng.loads(L.s[I], wi, ws + I), barrier, meet);
       __builtin_amdgcn_sched_barrier(0);
     };
     mx4_unroll(body, std::make_integer_sequence<int, NS>{});
@@ -653,10 +688,8 @@ struct F8GroupWork {
 
 template <class Eng, class Store, class Work>
 __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_f8_tiles(F8Problem p) {
-  __shared__ __attribute__((aligned(16))) char s0[Eng::STAGE];
-  __shared__ __attribute__((aligned(16))) char s1[Eng::STAGE];
-  __shared__ __attribute__((aligned(16))) char s2[Eng::NS > 2 ? Eng::STAGE : 16];
-  __shared__ __attribute__((aligned(16))) char s3[Eng::NS > 3 ? Eng::STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char a0[Eng::STAGE_A], b0[Eng::STAGE_B];
+  __shared__ __attribute__((aligned(16))) char a1[Eng::STAGE_A], b1[Eng::STAGE_B];
   __shared__ __attribute__((aligned(16))) char ep[Eng::EP];
   if constexpr (Eng::BROW) {   // where the scales decide, both kinds are launched, and one has the work
     if (p.powers) {
@@ -665,7 +698,7 @@ __global__ __launch_bounds__(Eng::NTHR, Eng::WAVES) void k_f8_tiles(F8Problem p)
     }
   }
   Work work(p);
-  f8_tiles<Eng, Store>(p, work, F8Lds{{s0, s1, s2, s3}, ep});
+  f8_tiles<Eng, Store>(p, work, F8Lds{{{a0, b0}, {a1, b1}}, ep});
 }
 
 }  // namespace qg
