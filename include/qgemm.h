@@ -526,6 +526,8 @@ qg_status qgemm_f8_grouped(const uint8_t *A, const float *A_scales, const int32_
  *     dX = RNE(value(D) . value(W)),  dW = RNE(value(D^T) . value(X^T)^T)
  *   D is quantized by rows for dX and its transpose by rows for dW, both as by
  *   qquantize_f8 (which makes XT and WT): the one rounding besides the results'.
+ *   Where all of XT's scales are normal powers of two, a large dW multiplies by the
+ *   scales' exponents, and products of scales outside of fp32's range stay exact.
  *   dH       device [m, inter], GU device [m, 2 inter], in dtype (QG_BF16 or QG_FP16)
  *   XT       device codes [k, R] of the transposed input, R = m rounded up to 16
  *            (values past m zeros), XT_scales by rows [blocks(m), k]; unused
@@ -535,12 +537,12 @@ qg_status qgemm_f8_grouped(const uint8_t *A, const float *A_scales, const int32_
  *   dX       device [m, k] in dx_dtype, or NULL;  dW device [2 inter, k] in
  *            dw_dtype, or NULL (both dtypes QG_BF16, QG_FP16 or QG_FP32; that of
  *            a NULL is not looked at)
- *   m == 0: dW, if wanted, is filled with zeros.
+ *   m == 0: dW, if wanted, is filled with zeros; inter == 0: dX is.
  *   Tile multiples: inter % 128 == 0, k % 16 == 0; inter at most 2^30 - 128.
  *   Alignment: matrices 16 bytes, scales 4.
  *   workspace: required, 256-byte aligned, at least
  *   qgated_f8_backward_workspace_size(m, inter, k) bytes (0 for sizes the call
- *   refuses and for m == 0).  Calls that share one must not overlap. */
+ *   refuses and for m == 0 or inter == 0).  Calls that share one must not overlap. */
 enum { QG_GATE_SILU = 0, QG_GATE_GELU = 1 };
 
 qg_status qgated_f8(const uint8_t *A, const float *A_scales, const uint8_t *B, const float *B_scales,

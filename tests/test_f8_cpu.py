@@ -115,7 +115,7 @@ def backward(**kw):
     (dict(dH=FAKE + 8), ALIGN), (dict(GU=FAKE + 8), ALIGN), (dict(XT=FAKE + 8), ALIGN), (dict(WT=FAKE + 8), ALIGN),
     (dict(dX=FAKE + 8), ALIGN), (dict(dW=FAKE + 8), ALIGN), (dict(XS=FAKE + 2), ALIGN), (dict(WS=FAKE + 2), ALIGN),
     (dict(), WORKSPACE), (dict(ws=FAKE, wsb=255), WORKSPACE), (dict(ws=FAKE + 16, wsb=1 << 30), ALIGN),
-    (dict(m=0, dW=None, dH=None), OK), (dict(inter=0), OK), (dict(dX=None, dW=None, dH=None), OK),
+    (dict(m=0, dW=None, dH=None), OK), (dict(inter=0, dX=None), OK), (dict(dX=None, dW=None, dH=None), OK),
     # what a NULL result does not need is not looked at
     (dict(dX=None, WT=None, WS=None, dxt=0), WORKSPACE), (dict(dW=None, XT=None, XS=None, dwt=0), WORKSPACE),
 ])

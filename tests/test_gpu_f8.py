@@ -532,6 +532,61 @@ def test_gated_backward_no_tokens():
         assert dx.shape == (0, 48) and dw.shape == (256, 48) and not dw.any()
 
 
+def test_gated_backward_no_channels():
+    # dX sums over none: zeros, whatever its memory held
+    dh, gu = torch.empty(5, 0, dtype=BF, device="cuda"), torch.empty(5, 0, dtype=BF, device="cuda")
+    xt, xts = codes8(np.zeros((48, 16), np.uint8)), dev(np.ones((1, 48), np.float32))
+    wt, wts = codes8(np.zeros((48, 0), np.uint8)), dev(np.zeros((1, 0), np.float32))
+    for t in (BF, SF):
+        spoil = torch.full((5, 48), float("nan"), dtype=t, device="cuda")
+        del spoil
+        dx, dw = qg.gated_f8_backward(dh, gu, xt, xts, wt, wts, dx_dtype=t)
+        assert dx.shape == (5, 48) and not dx.any() and dw.shape == (0, 48)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** -127, 2.0 ** -126, 2.0 ** 100, 3.0, -1.0, 0.0, float("inf"), float("nan")])
+def test_gated_backward_large_scales_at_the_ends(scale):
+    """One scale of XT among many, where it decides between two kernels: its column, and those beside it."""
+    m, inter, k = 1030, 2560, 7984
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)   # noqa: E731
+    dh, gu = r(m, inter), r(m, 2 * inter)
+    gu[:, 0], gu[:, inter], dh[:, 0] = 2.0, 0.0, 1.0           # du of channel 0: act(2) for every token
+    xt = codes8(np.full((k, 1040), 0x38, np.uint8))            # codes of 1
+    xts = torch.ones(9, k, device="cuda")
+    xts[3, 1000] = scale                                       # tokens 384 .. 511
+    _, dw = qg.gated_f8_backward(dh, gu, xt, xts, None, None, dw_dtype=SF)
+    code, row = ref.quantize(np.full((1, 16), ref.gate(np.array(2.0), "silu")[0]))
+    one = ref.values(code, row)[0, 0]
+    got = host(dw[inter])
+    beside = np.delete(got, 1000)
+    # at most m sums, each off by half a step
+    assert np.all(np.abs(beside - m * one) <= m * 2.0 ** -23 * m * one)
+    if np.isfinite(scale):
+        assert abs(got[1000] - (m - 128 + 128 * scale) * one) <= m * 2.0 ** -23 * (m - 128 + 128 * abs(scale)) * one
+    else:
+        assert not np.isfinite(got[1000]) and np.isnan(host(dw[0, 1000:1001])).all()   # 0 times it
+        assert torch.isfinite(dw[:, :1000]).all() and torch.isfinite(dw[:, 1001:]).all()
+
+
+@pytest.mark.parametrize("odd", [False, True])
+def test_gated_backward_large_bad_values(odd):
+    m, inter, k = 1030, 2560, 7984
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)   # noqa: E731
+    x, dh, gu = r(m, k), r(m, inter), r(m, 2 * inter)
+    *_, xt, xts = qg.quantize_f8(x, transposed=True)
+    if odd:
+        xts[0, 0] *= 1.5
+    _, dw0 = qg.gated_f8_backward(dh, gu, xt, xts, None, None)
+    dh[200, 30], dh[1029, 31] = float("nan"), float("inf")
+    _, dw = qg.gated_f8_backward(dh, gu, xt, xts, None, None)
+    for i in (30, 31):
+        assert torch.isnan(dw[[i, inter + i]]).all()
+    keep = torch.tensor([i for i in range(2 * inter) if i % inter not in (30, 31)], device="cuda")
+    assert torch.equal(dw[keep], dw0[keep])
+
+
 def test_gated_backward_bad_values_stay_in_their_rows():
     # a NaN in dH spoils its row's block of D: that row of dX, that channel's tokens in dW
     rng = np.random.default_rng(2)

@@ -861,6 +861,15 @@ def f8_workspace_size(m: int, n: int, k: int, b_block: int = 128) -> int:
     return int(lib().qgemm_f8_workspace_size(m, n, k, b_block))
 
 
+def _f8_need(size: str, dev: int, *args) -> int:
+    """Workspace bytes that the tensors' device asks for."""
+    fn = getattr(lib(), size)
+    if dev == _current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _f8_workspace(need: int, like: torch.Tensor, given: Optional[torch.Tensor]):
     """(tensor, address, bytes) of workspace: the caller's, else a fresh one
     when the library asks for any."""
@@ -892,7 +901,7 @@ def gemm_f8(A: torch.Tensor, A_scales: torch.Tensor, B: torch.Tensor, B_scales: 
     dev = _mx4_devices(f, (A, A_scales, B, B_scales, bias, out, workspace),
                        ("A", "A_scales", "B", "B_scales", "bias", "out", "workspace"))
     C = out if out is not None else A.new_empty((m, n), dtype=out_dtype)
-    need = lib().qgemm_f8_workspace_size(m, n, k, b_block) if workspace is None else 0
+    need = _f8_need("qgemm_f8_workspace_size", dev, m, n, k, b_block) if workspace is None else 0
     ws, ws_ptr, ws_bytes = _f8_workspace(need, A, workspace)
     _mx4_call(f, dev, A.data_ptr(), A_scales.data_ptr(), B.data_ptr(), B_scales.data_ptr(), _ptr(bias),
               C.data_ptr(), m, n, k, b_block, _CODES[out_dtype], QG_NONE if bias is None else _CODES[bias.dtype],
@@ -1018,7 +1027,7 @@ def gated_f8_backward(dH: torch.Tensor, GU: torch.Tensor, XT: Optional[torch.Ten
     dW = None if XT is None else dH.new_empty((2 * inter, k), dtype=dw_dtype)
     if k == 0:
         return dX, dW
-    need = lib().qgated_f8_backward_workspace_size(m, inter, k) if workspace is None else 0
+    need = _f8_need("qgated_f8_backward_workspace_size", dev, m, inter, k) if workspace is None else 0
     ws, ws_ptr, ws_bytes = _f8_workspace(need, dH, workspace)
     _mx4_call(f, dev, dH.data_ptr(), GU.data_ptr(), _ptr(XT), _ptr(XT_scales), _ptr(WT), _ptr(WT_scales), _ptr(dX),
               _ptr(dW), m, inter, k, code, _CODES[dH.dtype], 0 if dX is None else _CODES[dx_dtype],

@@ -598,8 +598,8 @@ qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT, 
                              int inter, int k, int act, qg_dtype dt, qg_dtype dx_dt, qg_dtype dw_dt,
                              void *workspace, size_t ws_bytes, void *stream) {
   if (m < 0 || inter < 0 || k <= 0) return QG_ERR_SHAPE;
-  if (inter == 0 || (m == 0 && !dW) || (!dX && !dW)) return QG_OK;   // nothing to compute
-  const bool some = m > 0;
+  if ((m == 0 || !dX) && (inter == 0 || !dW)) return QG_OK;   // nothing to compute
+  const bool some = m > 0 && inter > 0;
   if (some && (!dH || !GU || (dX && (!WT || !WTS)) || (dW && (!XT || !XTS)))) return QG_ERR_NULL;
   if (!act_ok(dt) || (dX && !f8_out_ok(dx_dt)) || (dW && !f8_out_ok(dw_dt))) return QG_ERR_DTYPE;
   if (!gate_ok(act)) return QG_ERR_MODE;
@@ -608,8 +608,11 @@ qg_status qgated_f8_backward(const void *dH, const void *GU, const uint8_t *XT, 
       !aligned(dX, 16) || !aligned(dW, 16) || !aligned(XTS, 4) || !aligned(WTS, 4))
     return QG_ERR_ALIGN;
   hipStream_t s = as_stream(stream);
-  if (!some)
-    return mx4_status(qg::launch_fill_zero(dW, static_cast<size_t>(2 * inter) * k * (dw_dt == QG_FP32 ? 4 : 2), s));
+  if (!some) {   // sums over no tokens (dW) or no channels (dX)
+    void *zero = m == 0 ? dW : dX;
+    const size_t n = m == 0 ? 2 * static_cast<size_t>(inter) : static_cast<size_t>(m);
+    return mx4_status(qg::launch_fill_zero(zero, n * k * ((m == 0 ? dw_dt : dx_dt) == QG_FP32 ? 4 : 2), s));
+  }
   const GatedWs ws(m, inter, k);
   if (!workspace || ws_bytes < ws.bytes) return QG_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return QG_ERR_ALIGN;
