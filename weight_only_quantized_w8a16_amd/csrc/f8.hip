@@ -1,9 +1,13 @@
 // f8.hip -- conversions of the block-scaled 8-bit float format (F8): quantize
 // (by rows or by 128 x 128 blocks, transposed as well), read back, and the
 // gradient of the gated block's activation and product, quantized both ways
-// as the two products of the backward pass read it.  All of them are bound by
-// HBM (the smallest by a launch): a value is read once and its codes are
-// written once each.
+// as the two products of the backward pass read it.  A value is read once and its codes are
+// written once each, so all of them are bound by HBM (5.2 TB/s in a large copy) or,
+// the smallest, by a launch.  Measured on MI355X, bf16, inputs out of the caches:
+//     rows 16 x 2048 2.4 us, 4000 x 3600 9.5 us (4.6 TB/s), 4096 x 3584 both ways 14.7 us (4.0),
+//     blocks of 18944 x 3584 both ways 47 us (5.8), read back 4096 x 3584 9.9 us (4.5).
+// Loads come first, all of a thread's in flight before one is used (both ways 17.4 -> 14.7 us),
+// and the division by a scale is part of the conversion instruction.
 #include <algorithm>
 
 #include "f8_common.hpp"
@@ -12,23 +16,27 @@ namespace qg {
 
 namespace {
 
-// Eight consecutive values of a row as fp32.
+// Eight consecutive values of a row, as loaded (zeros unless they are) and as fp32.
+// Apart, so that loads behind a bounds check are all in flight before the first is used.
 template <int DT>
-__device__ __forceinline__ void load8(const void *X, size_t i, float (&v)[8]) {
-  if constexpr (DT == QG_FP32) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(X) + i);
-    const f32x4 b = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(X) + i + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(X) + i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = bits_to_f32<DT>(static_cast<uint16_t>(a[e] & 0xFFFFu));
-      v[2 * e + 1] = bits_to_f32<DT>(static_cast<uint16_t>(a[e] >> 16));
+struct F8Eight {
+  u32x4 w[DT == QG_FP32 ? 2 : 1] = {};
+  __device__ __forceinline__ void load(const void *X, size_t i) {
+    if constexpr (DT == QG_FP32) {
+      w[0] = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(X) + i);
+      w[1] = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(X) + i + 4);
+    } else {
+      w[0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(X) + i);
     }
   }
-}
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (DT == QG_FP32) v[e] = __uint_as_float(w[e >> 2][e & 3]);
+      else v[e] = bits_to_f32<DT>(static_cast<uint16_t>(e & 1 ? w[0][e >> 1] >> 16 : w[0][e >> 1] & 0xFFFFu));
+    }
+  }
+};
 
 // The maximum over the 16 lanes of a DPP row, in all of them (all active).
 __device__ __forceinline__ int max16(int x) {
@@ -45,15 +53,17 @@ __global__ __launch_bounds__(256) void k_f8_rows(const void *X, uint8_t *Q, floa
   for (uint32_t g = blockIdx.x * 16 + (threadIdx.x >> 4); g < groups; g += gridDim.x * 16) {
     const uint32_t row = g / kb, b = g - row * kb, col = b * 128 + 8 * l;
     const size_t at = static_cast<size_t>(row) * k + col;
-    float v[8] = {};
-    if (col < k) load8<DT>(X, at, v);
+    F8Eight<DT> in;
+    float v[8];
+    if (col < k) in.load(X, at);
+    in.values(v);
     int top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = f8_top(top, v[e]);
     const F8Scale s(max16(top));
     if (col < k) {
-      uint32_t lo = f8_pack4(v[0] * s.inv, v[1] * s.inv, v[2] * s.inv, v[3] * s.inv);
-      uint32_t hi = f8_pack4(v[4] * s.inv, v[5] * s.inv, v[6] * s.inv, v[7] * s.inv);
+      uint32_t lo = f8_pack4(v[0], v[1], v[2], v[3], s.scale);
+      uint32_t hi = f8_pack4(v[4], v[5], v[6], v[7], s.scale);
       *reinterpret_cast<u32x2 *>(Q + at) = s.bad ? u32x2{0, 0} : u32x2{lo, hi};
     }
     if (l == 0) S[static_cast<size_t>(b) * rows + row] = s.scale;
@@ -69,6 +79,7 @@ __global__ __launch_bounds__(256) void k_f8_rows(const void *X, uint8_t *Q, floa
 struct F8TileLds {
   char codes[128 * 128];   // [column][row], 16-byte chunk c of column n at c ^ ((n / 8) % 8)
   int top[128];
+  float scale[128];
 };
 struct F8TileOut {
   uint8_t *Q;       // [rows, ldq] or null
@@ -96,15 +107,27 @@ __device__ __forceinline__ void f8_emit(const float (&v)[4][8], F8TileLds &L, co
     if ((t & 15) == 0) atomicMax(&L.top[0], m);
     __syncthreads();
   } else if constexpr (COLS) {
-    // The wave's 16 rows of a column: lanes 16 and 32 apart, then LDS.
+    // The wave's 16 rows of a column: lanes 32 and 16 apart trade halves of their
+    // columns, which leaves two to a lane, then LDS.
+    int m[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int m = f8_top(f8_top(f8_top(f8_top(0, v[0][e]), v[1][e]), v[2][e]), v[3][e]);
-      const auto half = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-      m = max(static_cast<int>(half[0]), static_cast<int>(half[1]));
-      const auto row = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-      m = max(static_cast<int>(row[0]), static_cast<int>(row[1]));
-      if ((t & 63) < 16) atomicMax(&L.top[c + e], m);
+    for (int e = 0; e < 8; ++e) m[e] = f8_top(f8_top(f8_top(f8_top(0, v[0][e]), v[1][e]), v[2][e]), v[3][e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const auto x = __builtin_amdgcn_permlane32_swap(m[e], m[e + 4], false, false);
+      m[e] = max(static_cast<int>(x[0]), static_cast<int>(x[1]));
+    }
+    const int q = (t >> 4) & 3, at = c + 2 * (q & 1) + 4 * (q >> 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const auto x = __builtin_amdgcn_permlane16_swap(m[e], m[e + 2], false, false);
+      atomicMax(&L.top[at + e], max(static_cast<int>(x[0]), static_cast<int>(x[1])));
+    }
+    __syncthreads();
+    if (t < 128) {
+      const float scale = F8Scale(L.top[t]).scale;
+      L.scale[t] = scale;
+      if (col0 + t < k) o.ST[t] = scale;
     }
     __syncthreads();
   }
@@ -114,8 +137,8 @@ __device__ __forceinline__ void f8_emit(const float (&v)[4][8], F8TileLds &L, co
       const F8Scale s(BLOCK ? L.top[0] : max16(rtop[p]));
       const int row = row0 + r + p;
       if (row < rows && col0 + c < k) {
-        const uint32_t lo = f8_pack4(v[p][0] * s.inv, v[p][1] * s.inv, v[p][2] * s.inv, v[p][3] * s.inv);
-        const uint32_t hi = f8_pack4(v[p][4] * s.inv, v[p][5] * s.inv, v[p][6] * s.inv, v[p][7] * s.inv);
+        const uint32_t lo = f8_pack4(v[p][0], v[p][1], v[p][2], v[p][3], s.scale);
+        const uint32_t hi = f8_pack4(v[p][4], v[p][5], v[p][6], v[p][7], s.scale);
         *reinterpret_cast<u32x2 *>(o.Q + static_cast<size_t>(row) * o.ldq + col0 + c) =
             s.bad ? u32x2{0, 0} : u32x2{lo, hi};
       }
@@ -126,11 +149,11 @@ __device__ __forceinline__ void f8_emit(const float (&v)[4][8], F8TileLds &L, co
   if constexpr (COLS) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const F8Scale s(L.top[BLOCK ? 0 : c + e]);
-      const uint32_t w = f8_pack4(v[0][e] * s.inv, v[1][e] * s.inv, v[2][e] * s.inv, v[3][e] * s.inv);
-      *reinterpret_cast<uint32_t *>(L.codes + (c + e) * 128 + (((r >> 4) ^ (t & 7)) << 4) + (r & 15)) = s.bad ? 0 : w;
+      const float scale = BLOCK ? F8Scale(L.top[0]).scale : L.scale[c + e];
+      const uint32_t w = f8_pack4(v[0][e], v[1][e], v[2][e], v[3][e], scale);
+      *reinterpret_cast<uint32_t *>(L.codes + (c + e) * 128 + (((r >> 4) ^ (t & 7)) << 4) + (r & 15)) = scale == scale ? w : 0;
     }
-    if (BLOCK ? t == 0 : t < 128 && col0 + t < k) o.ST[t] = F8Scale(L.top[t]).scale;
+    if (BLOCK && t == 0) o.ST[0] = F8Scale(L.top[0]).scale;
     __syncthreads();
     const int padded = f8_pad16(rows);
 #pragma unroll
@@ -153,10 +176,13 @@ __global__ __launch_bounds__(512) void k_f8_tile(const void *X, uint8_t *Q, floa
   const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
   const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
   const size_t base = static_cast<size_t>(x) * rows * k;
-  float v[4][8] = {};
+  F8Eight<DT> from[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p)
-    if (row0 + r + p < rows && col0 + c < k) load8<DT>(X, base + static_cast<size_t>(row0 + r + p) * k + col0 + c, v[p]);
+    if (row0 + r + p < rows && col0 + c < k) from[p].load(X, base + static_cast<size_t>(row0 + r + p) * k + col0 + c);
+  float v[4][8];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) from[p].values(v[p]);
   const size_t pad = f8_pad16(rows);
   const F8TileOut o{
       ROWS ? Q + base : nullptr,
@@ -171,9 +197,13 @@ __global__ __launch_bounds__(512) void k_f8_tile(const void *X, uint8_t *Q, floa
 // Workgroups past the tiles (with columns) look through the other scales of the
 // weight gradient's product: powers[i] = 0 if the i-th of kF8Flags parts holds normal powers
 // of two alone (D's own are).
-template <int DT, bool ROWS, bool COLS>
+// 4096 x 18944 moves 776 MB, 150 us at a copy's rate; some 200 here, since one
+// workgroup of 8 waves fits a CU (197 registers: both gradients and the loads) and its loading,
+// arithmetic (25 instructions a value) and storing overlap with nobody's.  Bounding the registers
+// for two spills them (317 -> 584 us with both products of 16 columns).
+template <int DT, int ACT, bool ROWS, bool COLS>
 __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const void *GU, uint8_t *D, float *SD,
-                                                       uint8_t *DT_, float *SDT, int rows, int inter, int act,
+                                                       uint8_t *DT_, float *SDT, int rows, int inter,
                                                        const float *scales, size_t n_scales, uint32_t *powers,
                                                        int halves) {
   __shared__ __attribute__((aligned(16))) F8TileLds L;
@@ -192,28 +222,36 @@ __global__ __launch_bounds__(512) void k_f8_gated_grad(const void *dH, const voi
       return;
     }
   }
-  // halves 2: a workgroup for each half, where there are few.
+  // halves 2: a workgroup for each half, where there are few (100 x 1408 14 -> 9.6 us, as many
+  // loads again).
   const uint32_t tile = blockIdx.x / halves, ri = tile / kb, b = tile - ri * kb;
   const int first = halves == 2 ? static_cast<int>(blockIdx.x & 1) : 0, last = halves == 2 ? first : 1;
   const int row0 = static_cast<int>(ri) * 128, col0 = static_cast<int>(b) * 128;
   const int r = 4 * (threadIdx.x >> 4), c = 8 * (threadIdx.x & 15);
   const size_t wide = 2 * static_cast<size_t>(inter), pad = f8_pad16(rows);
-  float dg[4][8] = {}, du[4][8] = {};
+  F8Eight<DT> fh[4], fg[4], fu[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const size_t row = static_cast<size_t>(row0 + r + p);
     if (row0 + r + p < rows) {
-      float h[8], g[8], u[8];
-      load8<DT>(dH, row * inter + col0 + c, h);
-      load8<DT>(GU, row * wide + col0 + c, g);
-      load8<DT>(GU, row * wide + inter + col0 + c, u);
+      fh[p].load(dH, row * inter + col0 + c);
+      fg[p].load(GU, row * wide + col0 + c);
+      fu[p].load(GU, row * wide + inter + col0 + c);
+    }
+  }
+  float dg[4][8], du[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float value;
-        const float slope = f8_gate_slope(g[e], act, value);
-        dg[p][e] = h[e] * u[e] * slope;
-        du[p][e] = h[e] * value;
-      }
+  for (int p = 0; p < 4; ++p) {
+    float h[8], g[8], u[8];
+    fh[p].values(h);
+    fg[p].values(g);
+    fu[p].values(u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float value;
+      const float slope = f8_gate_slope(g[e], ACT, value);
+      dg[p][e] = h[e] * u[e] * slope;
+      du[p][e] = h[e] * value;
     }
   }
 #pragma unroll
@@ -314,7 +352,7 @@ hipError_t dequant_as(const uint8_t *Q, const float *S, void *out, int stack, in
   return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, int ACT>
 hipError_t grad_as(const F8GatedGrad &g, hipStream_t s) {
   uint64_t tiles = static_cast<uint64_t>(f8_blocks(g.m)) * (g.inter >> 7);
   const int halves = tiles <= static_cast<uint64_t>(device_cus()) ? 2 : 1;
@@ -322,8 +360,8 @@ hipError_t grad_as(const F8GatedGrad &g, hipStream_t s) {
   if ((tiles + kF8Flags) * 512 > kLaunch) return hipErrorNotSupported;
   const dim3 grid(static_cast<unsigned>(tiles) + (g.DT ? kF8Flags : 0)), block(512);
 #define QG_F8_GRAD(ROWS, COLS)                                                                                   \
-  hipLaunchKernelGGL((k_f8_gated_grad<DT, ROWS, COLS>), grid, block, 0, s, g.dH, g.GU, g.D, g.SD, g.DT, g.SDT, g.m, \
-                     g.inter, g.act, g.scales, g.n_scales, g.powers, halves)
+  hipLaunchKernelGGL((k_f8_gated_grad<DT, ACT, ROWS, COLS>), grid, block, 0, s, g.dH, g.GU, g.D, g.SD, g.DT, g.SDT, g.m, \
+                     g.inter, g.scales, g.n_scales, g.powers, halves)
   if (g.D && g.DT) QG_F8_GRAD(true, true);
   else if (g.D) QG_F8_GRAD(true, false);
   else QG_F8_GRAD(false, true);
@@ -358,7 +396,8 @@ hipError_t launch_fill_zero(void *p, size_t bytes, hipStream_t s) {
 }
 
 hipError_t launch_gated_f8_grad(const F8GatedGrad &g, hipStream_t s) {
-  return g.dt == QG_FP16 ? grad_as<QG_FP16>(g, s) : grad_as<QG_BF16>(g, s);
+  if (g.act == QG_GATE_GELU) return g.dt == QG_FP16 ? grad_as<QG_FP16, QG_GATE_GELU>(g, s) : grad_as<QG_BF16, QG_GATE_GELU>(g, s);
+  return g.dt == QG_FP16 ? grad_as<QG_FP16, QG_GATE_SILU>(g, s) : grad_as<QG_BF16, QG_GATE_SILU>(g, s);
 }
 
 }  // namespace qg

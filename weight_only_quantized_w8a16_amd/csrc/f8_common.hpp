@@ -21,14 +21,13 @@ __host__ __device__ constexpr int f8_pad16(int x) { return (x + 15) / 16 * 16; }
 // 17 binades below 448 stay as they are but for one.  It makes x / 2^e exact,
 // so a code is x's nearest whichever precision computes it.
 struct F8Scale {
-  float scale, inv;
+  float scale;
   bool bad;
   __device__ __forceinline__ explicit F8Scale(int top) {
     int e = max((top >> 23) - 135 + ((top & 0x7FFFFF) > 0x600000 ? 1 : 0), -126);
     e = top == 0 ? 0 : e;
     bad = top >= 0x7F800000;
     scale = bad ? __builtin_nanf("") : __int_as_float((e + 127) << 23);
-    inv = __int_as_float((127 - e) << 23);   // not used where bad
   }
 };
 // Whether a scale is a normal power of two, as the matrix instruction's own are.
@@ -38,10 +37,11 @@ __device__ __forceinline__ bool f8_power(float s) {
 }
 __device__ __forceinline__ int f8_top(int top, float v) { return max(top, __float_as_int(v) & 0x7FFFFFFF); }
 
-// Four values of at most 448 in magnitude -> codes, rounded to nearest even.
-__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+// Four values / scale (a power of two; at most 448 then) -> codes, rounded to nearest even.
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d, float scale) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  const s16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(s16x2{0, 0}, a, b, scale, false);
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, c, d, scale, true));
 }
 // Two codes of a word (its low or high half) -> values, exact.
 template <bool HIGH>
