@@ -1,5 +1,6 @@
 """Weight-only quantized GEMM (fpA_intB: W4A16 groupwise, W8A16 per channel,
-top-k MoE, and microscaled 4-bit floats, MX4) for AMD MI355X (gfx950).
+top-k MoE, microscaled 4-bit floats, MX4, and block-scaled 8-bit floats, F8)
+for AMD MI355X (gfx950).
 
 Thin torch-facing wrappers over the C ABI in ``include/qgemm.h``: they check
 tensor placement, flatten leading dimensions, pass raw device pointers and
