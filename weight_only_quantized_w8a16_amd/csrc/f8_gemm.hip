@@ -285,7 +285,9 @@ struct F8Plan {
 // timings on MI355X, 16 to 4096 rows and 13 weight shapes of 512 x 8192 to 18944 x
 // 3584, dense and gated, each tile and slice count forced, and 90 with B's scales by
 // rows (residual 8 and 6 %); the tile so picked is within 0.4 % of the best one on
-// average, 20 % at worst (100 x 3584 x 3584 in eight slices instead of three).
+// average, 20 % at worst (100 x 3584 x 3584 in eight slices instead of three).  The
+// steps of the 256 x 256 tile by blocks were 4 % longer then and are scaled by what they
+// take since.
 struct F8Cost {
   int tile, bm, bn, most;
   float t0, lone, shared, full, again;
@@ -454,7 +456,8 @@ hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s) {
     p.slices = pl.slices;
   }
   // Two launches, of which the scales let one have the work, pay from some 50 us
-  // on (4096 x 18944 x 3584 dB 889 -> 732 us; the idle one takes 4).
+  // on (4096 x 18944 x 3584 dB 889 -> 732 us with the gradient's kernel; the idle one
+  // takes 4.7).
   if (static_cast<double>(a.M) * a.N * a.K < 4e10) p.powers = nullptr;
   switch (a.out) {
     case QG_FP32: return run_f8<QG_FP32>(p, form, brow, pl.tile, s);
