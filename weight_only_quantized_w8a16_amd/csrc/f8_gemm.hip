@@ -4,7 +4,8 @@
 // act(g) * u) (include/qgemm.h).
 //
 // The scales are any fp32 numbers, so they cannot ride on the matrix
-// instruction (whose own are powers of two).  Scales change every 128 k, and
+// instruction (whose own are powers of two), but for the weight's gradient, where
+// a kernel has looked through them before.  Scales change every 128 k, and
 // one 16 x 16 x 128 instruction covers just that: it multiplies on zero, and its
 // sum t is added as acc += t * (sa * sb) in fp32, four instructions of a lane
 // for every matrix instruction.  The instruction sums eight consecutive k at a
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(512) void k_f8_stream(F8Problem p, int slab0) {
   }
 }
 
-// K slices: C = RNE_out(the slices' partials summed in slice order + bias).
+// K slices: C = RNE_out(the slices' partials summed in slice order + bias).  Bound by
+// the partials' way through the 256 MB cache: 6 slices of 333 x 3584 6.6 us.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_f8_reduce(F8Problem p) {
   const size_t mn = static_cast<size_t>(p.M) * p.N, step = static_cast<size_t>(gridDim.x) * 1024;
