@@ -61,6 +61,30 @@ struct F8Problem {
   const uint32_t *powers; // kF8Flags words, 0: all scales are normal powers of two; or null: not known
 };
 
+// A lane's part of a wave's loads from A or B.  Load i brings rows 8 i .. 8 i + 7 of the
+// wave's, 128 bytes each, lane l row 8 i + l / 8, placed chunk l % 8 (the swizzle above;
+// odd loads' rows differ from even ones' by 8).  The whole offset goes into the vector
+// register, which a buffer resource checks against its size: the scalar offset may be
+// left out of that check, so a resource that ends within the wave's rows would not
+// bound loads whose rows are in it.  (Rows as scalar offsets: 4096 x 18944 x 3584 the same
+// 266 us, dW by powers of two of that size with its gradient 712 us for 723; rows in the
+// resource's base, one for two loads: 268 for 258 and 728 for 723.)
+struct F8LaneLoads {
+  static constexpr uint32_t kOutside = 0x80000000u;   // past every resource
+  uint32_t chunk[2], off[2];
+  __host__ __device__ constexpr F8LaneLoads(int lane, uint32_t K) : chunk{}, off{} {
+    for (int x = 0; x < 2; ++x) {
+      chunk[x] = static_cast<uint32_t>((lane & 7) ^ ((4 * x + (lane >> 4)) & 7)) << 4;
+      off[x] = (8u * static_cast<uint32_t>(x) + static_cast<uint32_t>(lane >> 3)) * K + chunk[x];
+    }
+  }
+  // Of loads 0 and 1, with `rem` bytes left of every row; load i is past(i) further.
+  __host__ __device__ constexpr uint32_t start(int x, int rem) const {
+    return static_cast<int>(chunk[x]) < rem ? off[x] : kOutside;
+  }
+  static __host__ __device__ constexpr uint32_t past(int i, uint32_t K) { return 16u * static_cast<uint32_t>(i >> 1) * K; }
+};
+
 // A stage: A's rows and the scales, and B's rows.
 struct F8Stage {
   char *a, *b;
@@ -100,19 +124,16 @@ struct F8Engine {
 
   const F8Problem &p;
   const int lane, wave, wm, wn, nl, q, kb;
-  uint32_t lane_off[2];
-  int chunk[2], a_addr[2], b_addr[2];
+  const F8LaneLoads lane_loads;
+  int a_addr[2], b_addr[2];
   uint32_t scale_at, scale_step, scale_cut;   // a lane's byte offset; bytes from step to step, and of these off the end
   f32x4 acc[TM][TN];
 
   __device__ __forceinline__ F8Engine(const F8Problem &pr, int wave_)
       : p(pr), lane(threadIdx.x & 63), wave(wave_), wm(wave / WN), wn(wave % WN), nl(lane & 15), q(lane >> 4),
-        kb(f8_blocks(pr.K)) {
-    // Load i of a wave brings 8 rows, lane l row l / 8, placed chunk l % 8.
+        kb(f8_blocks(pr.K)), lane_loads(lane, static_cast<uint32_t>(pr.K)) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      chunk[x] = ((lane & 7) ^ ((4 * x + (lane >> 4)) & 7)) << 4;
-      lane_off[x] = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.K) + chunk[x];
       a_addr[x] = (wm * WTM + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
       b_addr[x] = (wn * WTN + nl) * 128 + (((4 * x + q) ^ (nl >> 1)) << 4);
     }
@@ -159,8 +180,6 @@ struct F8Engine {
     }
   }
 
-  static constexpr uint32_t kOutside = 0x80000000u;   // past every resource
-
   // Channel of row r of a tile's part of B, the tile's columns from col_lo on.
   __device__ __forceinline__ int channel(int col_lo, int r) const {
     if constexpr (GATED) {
@@ -172,8 +191,7 @@ struct F8Engine {
     }
   }
 
-  // One step's loads: one resource for the wave's rows and one for its channels, the
-  // loads' rows as scalar offsets (which count for its bounds, too).
+  // One step's loads: one resource for the wave's rows and one for its channels.
   struct Loads {
     const void *a, *b, *s;
     uint32_t a_bytes, b_bytes, s_bytes, off[2];
@@ -187,7 +205,7 @@ struct F8Engine {
     const int rem = p.K - step * 128;   // bytes of the rows left
     Loads l;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) l.off[x] = chunk[x] < rem ? lane_off[x] : kOutside;
+    for (int x = 0; x < 2; ++x) l.off[x] = lane_loads.start(x, rem);
     l.a = t.a + k0;
     l.b = t.b + k0;
     l.s = reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step;
@@ -200,11 +218,14 @@ struct F8Engine {
   static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, static_cast<int>(bytes), kRsrcFlags);
   }
+  __device__ __forceinline__ int offset(const Loads &l, int i) const {
+    return static_cast<int>(l.off[i & 1] + F8LaneLoads::past(i, static_cast<uint32_t>(p.K)));
+  }
   __device__ __forceinline__ void issue_a(const Loads &l, int from, int to) const {
 #pragma unroll
     for (int i = from; i < to; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.a, l.a_bytes), lds_ptr(l.stage.a + (wave * A_DMA + i) * 1024), 16,
-                                               static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
+                                               offset(l, i), 0, 0, 0);
   }
   __device__ __forceinline__ void issue_scales(const Loads &l) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.s, l.s_bytes), lds_ptr(l.stage.a + STAGE_S + scale_load() * 256), 4,
@@ -214,7 +235,7 @@ struct F8Engine {
 #pragma unroll
     for (int i = 0; i < B_DMA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc(l.b, l.b_bytes), lds_ptr(l.stage.b + (wave * B_DMA + i) * 1024), 16,
-                                               static_cast<int>(l.off[i & 1]), 8 * i * p.K, 0, 0);
+                                               offset(l, i), 0, 0, 0);
   }
   __device__ __forceinline__ void issue(const Loads &l) const {
     issue_b(l);
