@@ -49,3 +49,10 @@ static_assert(all(16, 0) && all(112, 0) && all(128, 0) && all(272, 0) && all(272
 // the longest rows that the tiles take: 256 of them below 2^31 bytes
 static_assert(all((1u << 23) - 16, 0) && all((1u << 23) - 16, (1 << 23) - 128), "long rows");
 ''')
+
+
+def test_scales_past_32_bits(tmp_path):
+    assert_compiles(tmp_path, r'''
+static_assert(f8_scale_offset(1, 1u << 30) * sizeof(float) == size_t(1) << 32, "2^30 rows");
+static_assert(f8_scale_offset(3, (1u << 31) - 256) == 3 * ((size_t(1) << 31) - 256), "the most rows");
+''')

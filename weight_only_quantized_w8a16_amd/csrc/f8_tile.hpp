@@ -85,6 +85,10 @@ struct F8LaneLoads {
   static __host__ __device__ constexpr uint32_t past(int i, uint32_t K) { return 16u * static_cast<uint32_t>(i >> 1) * K; }
 };
 
+// The first scale of a step among scales that are `per` apart from step to step: 2^30
+// rows and more have a step's scales past 2^32 bytes.
+__host__ __device__ constexpr size_t f8_scale_offset(int step, uint32_t per) { return static_cast<size_t>(step) * per; }
+
 // A stage: A's rows and the scales, and B's rows.
 struct F8Stage {
   char *a, *b;
@@ -126,7 +130,7 @@ struct F8Engine {
   const int lane, wave, wm, wn, nl, q, kb;
   const F8LaneLoads lane_loads;
   int a_addr[2], b_addr[2];
-  uint32_t scale_at, scale_step, scale_cut;   // a lane's byte offset; bytes from step to step, and of these off the end
+  uint32_t scale_at, scale_step, scale_cut;   // a lane's byte offset; scales from step to step, bytes of them off the end
   f32x4 acc[TM][TN];
 
   __device__ __forceinline__ F8Engine(const F8Problem &pr, int wave_)
@@ -143,13 +147,13 @@ struct F8Engine {
     const int r = scale_load() * 64 + lane;
     if (r < BM) {
       scale_at = static_cast<uint32_t>(r) * 4u;
-      scale_step = static_cast<uint32_t>(p.M) * 4u;
+      scale_step = static_cast<uint32_t>(p.M);
     } else if (BROW) {
       scale_at = static_cast<uint32_t>(r - BM) * 4u;
-      scale_step = static_cast<uint32_t>(p.N) * 4u;
+      scale_step = static_cast<uint32_t>(p.N);
     } else {
       scale_at = static_cast<uint32_t>(channel(0, r - BM) >> 7) * static_cast<uint32_t>(kb) * 4u;
-      scale_step = 4u;
+      scale_step = 1u;
     }
     scale_step = __builtin_amdgcn_readfirstlane(scale_step);
     scale_cut = scale_load() < BM / 64 || BROW ? 0u : 4u;
@@ -208,7 +212,7 @@ struct F8Engine {
     for (int x = 0; x < 2; ++x) l.off[x] = lane_loads.start(x, rem);
     l.a = t.a + k0;
     l.b = t.b + k0;
-    l.s = reinterpret_cast<const char *>(t.scales) + static_cast<size_t>(step) * scale_step;
+    l.s = t.scales + f8_scale_offset(step, scale_step);
     l.a_bytes = t.a_bytes ? t.a_bytes - k0 : 0u;
     l.b_bytes = t.b_bytes ? t.b_bytes - k0 : 0u;
     l.s_bytes = step_ < t.s1 ? t.scale_bytes - static_cast<uint32_t>(step) * scale_cut : 0u;
