@@ -107,3 +107,59 @@ def test_streamed_gated_of_many_channels(m, groups, act, dtype):
     inter = 128 * (4 * cus() // (8 * groups) + 1)
     assert inter // 16 * groups > 4 * cus()
     check_gated(m, inter, 272, act, dtype, m)
+
+
+# -- several tiles a workgroup ---------------------------------------------------------
+
+# rows, and the tile's: more tiles than workgroups (two a CU but for the largest)
+MANY = [("T256", 2100, 256), ("T128", 1100, 128), ("T64", 600, 64)]
+
+
+@pytest.mark.parametrize("k", [16, 272, 400])     # one step, an odd number, an even one
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", [BF, SF])
+@pytest.mark.parametrize("tile,m,rows", MANY)
+def test_gated_of_many_tiles(tile, m, rows, act, dtype, k):
+    qg.set_override(f8_tile=tile)
+    inter, cols = (9216, 128) if tile == "T256" else (9216, 64)
+    assert -(-m // rows) * (inter // cols) > 2 * cus()
+    check_gated(m, inter, k, act, dtype, k)
+
+
+@pytest.mark.parametrize("k", [16, 272, 400])
+@pytest.mark.parametrize("dtype", [BF, SF])
+@pytest.mark.parametrize("tile,m,rows", MANY)
+def test_by_expert_of_many_tiles(tile, m, rows, dtype, k):
+    # experts without rows, with one, with a whole tile and with several; n past the last whole tile; rows of no expert
+    qg.set_override(f8_tile=tile)
+    rng = np.random.default_rng(k)
+    sizes = [0, m // 3 + 1, 0, 0, 1, rows, m // 5, 0, rows + 1, m // 4, 0]
+    E, n = len(sizes), 9232
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32) + 3
+    total = int(off[-1]) + 5
+    cols, most = (256, 1) if tile == "T256" else (128, 2)      # workgroups a CU
+    assert sum(-(-s // rows) for s in sizes) * -(-n // cols) > most * cus()
+    a, sa, av = exact_pair(rng, total, k, 1)
+    b, sb, bv = exact_pair(rng, n, k, 128, (E,))
+    bias = torch.from_numpy(rng.integers(-8, 9, (E, n)) / 4.0).to(BF).cuda()
+    want = torch.full((total, n), 77.0, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        want[off[e]:off[e + 1]] = av[off[e]:off[e + 1]] @ bv[e].t() + bias[e].double()
+    for _ in range(2):
+        out = torch.full((total, n), 77.0, dtype=dtype, device="cuda")
+        same(qg.gemm_f8_grouped(a, sa, torch.from_numpy(off).cuda(), b, sb, bias=bias, out=out), want)
+
+
+@pytest.mark.parametrize("tile", TILES)
+def test_by_expert_of_many_experts_and_tiles(tile):
+    # a workgroup's tiles lie in several lots of 64 experts
+    qg.set_override(f8_tile=tile)
+    rng = np.random.default_rng(3)
+    E, n, k = 300, 528, 144
+    sizes = rng.integers(0, 4, E)
+    sizes[[5, 150, 299]] = 70, 300, 129
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    a, sa, av = exact_pair(rng, int(off[-1]), k, 1)
+    b, sb, bv = exact_pair(rng, n, k, 128, (E,))
+    want = torch.cat([av[off[e]:off[e + 1]] @ bv[e].t() for e in range(E)])
+    same(qg.gemm_f8_grouped(a, sa, torch.from_numpy(off).cuda(), b, sb, out_dtype=SF), want)
