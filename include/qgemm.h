@@ -510,7 +510,7 @@ qg_status qgemm_f8_grouped(const uint8_t *A, const float *A_scales, const int32_
  * B[inter .. 2 inter):
  *     H[m, i] = RNE_out(act(g) * u),   act(g) = g * sigmoid(y),
  *     QG_GATE_SILU: y = g;   QG_GATE_GELU (its tanh form): y = 2 sqrt(2 / pi)
- *     (g + 0.044715 g^3)
+ *     (g + 0.044715 g^3);  a sigmoid below 2^-126 counts as 0, here and in act'
  *   A        device codes [m, k], A_scales by rows [blocks(k), m]
  *   B        device codes [2 inter, k], the gate's channels before the up
  *            projection's, B_scales by blocks [2 inter / 128, blocks(k)]

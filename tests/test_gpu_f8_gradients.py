@@ -1,5 +1,5 @@
 """The F8 gated block's gradients against differences, by a bound that no gradient of
-another size or sign meets."""
+another size or sign meets, and its values where the sigmoid is tiny."""
 import numpy as np
 import pytest
 import torch
@@ -83,3 +83,21 @@ def test_gradients_against_differences(act):
         bound += 1e-6 * norm(want)      # the differences' own error: e^2 / 6 of third derivatives, 2^-53 / e
         assert bound < norm(want) / 2   # so zeros, a wrong sign or half of it would not do
         assert norm(got - want) <= bound
+
+
+@pytest.mark.parametrize("act,low,high", [("silu", 80, 112), ("gelu", 5, 14)])
+def test_gates_whose_sigmoid_is_tiny(act, low, high):
+    """g = -s, u = s, down to sigmoids far below the smallest normal number, which may count as zeros."""
+    inter, k, m = 128, 16, 257
+    s = np.linspace(low, high, m).astype(np.float32)
+    ca = ref.encode(np.ones((m, 1)) * np.eye(1, k))
+    cb = ref.encode(np.concatenate([-np.ones((inter, 1)), np.ones((inter, 1))]) * np.eye(1, k))
+    h = qg.gated_f8(dev(ca).view(F8), dev(s[None]), dev(cb).view(F8), torch.ones(2, 1, device="cuda"), act, SF)
+    g = -s.astype(np.float64)
+    y = g if act == "silu" else np.sqrt(8 / np.pi) * (g + 0.044715 * g ** 3)
+    want = g / (1 + np.exp(-y)) * s
+    # the sigmoid: 5 roundings of y, the exponential's argument's and 2 of its own, the reciprocal's, doubled,
+    # or all of it below 2^-126; two products in fp32, whose subnormals have steps of 2^-149
+    tol = (7 * np.abs(y) + 10) * 2.0 ** -23 * np.abs(want) + 2.0 ** -126 * np.abs(g * s) + 2.0 ** -148 * (1 + s)
+    err = np.abs(h.double().cpu().numpy() - want[:, None])
+    assert (err <= tol[:, None]).all(), (err / tol[:, None]).max()

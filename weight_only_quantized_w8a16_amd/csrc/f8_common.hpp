@@ -52,7 +52,8 @@ __device__ __forceinline__ f32x2 f8_unpack2(uint32_t w) {
 
 // The gate: act(g) = g s with s = sigmoid(y), y = g (silu) or
 // 2 sqrt(2 / pi) (g + 0.044715 g^3) (gelu, in its tanh form: (1 + tanh(y / 2)) / 2
-// = s).  The sigmoid keeps its relative precision where 1 + tanh cancels.
+// = s).  The sigmoid keeps its relative precision where 1 + tanh cancels, down to 2^-126;
+// below (y < -87.3) the reciprocal gives 0, an error of g 2^-126 at most.
 // act'(g) = s + g s (1 - s) y'; where s (1 - s) is 0 the second term is, though
 // y' may be infinite.
 constexpr float kGelu = 1.5957691216057308f;
