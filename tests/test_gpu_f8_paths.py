@@ -163,3 +163,21 @@ def test_by_expert_of_many_experts_and_tiles(tile):
     b, sb, bv = exact_pair(rng, n, k, 128, (E,))
     want = torch.cat([av[off[e]:off[e + 1]] @ bv[e].t() for e in range(E)])
     same(qg.gemm_f8_grouped(a, sa, torch.from_numpy(off).cuda(), b, sb, out_dtype=SF), want)
+
+
+# -- the kernel taken ------------------------------------------------------------------
+
+@pytest.mark.parametrize("m,n,k", [(1, 26624, 2048), (16, 37888, 3584), (16, 131072, 512)])
+def test_one_slab_of_rows_is_streamed(m, n, k):
+    """Up to 16 rows tiles of their own steps are slower: the bits are those of the streaming kernel, whose
+    sums run in another order than a tile's."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    r = lambda *s: torch.rand(s, generator=g, device="cuda") + 0.5   # noqa: E731
+    codes = lambda *s: (torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8) & 0xB7).view(F8)  # noqa: E731
+    args = (codes(m, k), r(k // 128, m), codes(n, k), r(n // 128, k // 128))
+    calls = (lambda: qg.gemm_f8(*args, out_dtype=SF), lambda: qg.gated_f8(*args, out_dtype=SF))
+    got = [c() for c in calls]
+    qg.set_override(f8_tile="stream")
+    assert all(torch.equal(a, c()) for a, c in zip(got, calls))
+    qg.set_override(f8_tile="T64")
+    assert not any(torch.equal(a, c()) for a, c in zip(got, calls))

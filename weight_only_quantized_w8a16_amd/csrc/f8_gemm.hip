@@ -323,6 +323,12 @@ float tiles_time(const F8Cost &c, float tiles, int steps) {
 // row slab of its own for each in the streaming kernel, which so is taken for few rows
 // on few experts (8 experts, n = 3584, k = 2560: 4 rows 11.6 us against 15.8, 8 rows
 // 17.1 against 16.3; 64 experts, n = 2816, k = 2048: 32 rows 31.4 against 30.8).
+// Up to 16 rows, where either kernel reads every weight from memory once, no whole tiles
+// are taken: their steps wait for memory longer than the fit, of 16 rows and more, has it
+// (us, streamed against 64 x 128: 1 x 26624 x 2048 11.9 and 17.2, 16 x 37888 x 3584 25.6
+// and 31.8, 16 x 131072 x 512 14.7 and 16.3, gated 1 x 13312 x 2048 11.8 and 17.4, 16 x
+// 17920 x 720 10.8 and 12.8; 17 rows, streamed in two slabs: 37888 x 3584 46.9 and 32.0).
+// K slices are (9 x 512 x 18944 16.8 streamed, 14.3 in slices).
 F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
   const int steps = f8_blocks(K);
   F8Plan pl{kF8Stream, steps, 1, 0};
@@ -344,7 +350,8 @@ F8Plan plan_f8(int M, int N, int K, bool brow, int form, int E) {
       const float tiles = static_cast<float>(n / cols + (n % cols != 0)) *
                           (form == kGrouped ? static_cast<float>(M) / static_cast<float>(c.bm) + 0.5f * experts
                                             : static_cast<float>(M / c.bm + (M % c.bm != 0)));
-      for (int sl = 1; sl <= 16 && (sl == 1 || (form == kDense && sl <= steps / 2)); ++sl) {
+      const int least = M <= 16 && form != kGrouped ? 2 : 1;
+      for (int sl = least; sl <= 16 && (sl == 1 || (form == kDense && sl <= steps / 2)); ++sl) {
         const int kseg = (steps + sl - 1) / sl;
         if ((steps + kseg - 1) / kseg != sl) continue;
         float t = std::max(tiles_time(c, tiles * static_cast<float>(sl), kseg), c.t0 + read);
