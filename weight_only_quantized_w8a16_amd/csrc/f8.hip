@@ -3,9 +3,11 @@
 // gradient of the gated block's activation and product, quantized both ways
 // as the two products of the backward pass read it.  A value is read once and its codes are
 // written once each, so all of them are bound by HBM (5.2 TB/s in a large copy) or,
-// the smallest, by a launch.  Measured on MI355X, bf16, inputs out of the caches:
-//     rows 16 x 2048 2.4 us, 4000 x 3600 9.5 us (4.6 TB/s), 4096 x 3584 both ways 14.7 us (4.0),
-//     blocks of 18944 x 3584 both ways 47 us (5.8), read back 4096 x 3584 9.9 us (4.5).
+// the smallest, by a launch.  Measured on MI355X, bf16, all but the smallest's values out of the caches:
+//     rows 16 x 2048 2.1 us, 4000 x 3600 11.9 us (3.6 TB/s), 4096 x 3584 both ways 16.6 us (3.5),
+//     blocks of 18944 x 3584 both ways 55 us (5.0), read back 4096 x 3584 12.1 us (3.6);
+// with every call's results over the last one's, which the 256 MB cache then takes in part:
+// 11.3, 14.7, 48.5 (5.6 TB/s, past the copy's) and 11.3 us.
 // Loads come first, all of a thread's in flight before one is used (both ways 17.4 -> 14.7 us),
 // and the division by a scale is part of the conversion instruction.
 #include <algorithm>

@@ -48,7 +48,7 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 // Streaming kernel, for few rows: a workgroup owns 16 rows and NT tiles of 16
 // columns (gated: NT / 2 gate tiles and the up tiles beside them), and its waves
 // take 128-k blocks in turn.  Nothing is shared between waves until their sums
-// meet in LDS.  Bound by HBM: 1 x 131072 x 2048 (268 MB) 43.5 us, 6.2 TB/s.  Loads of
+// meet in LDS.  Bound by HBM: 1 x 131072 x 2048 (268 MB) 43.5 us, 6.2 TB/s, of 6.6 for a plain read.  Loads of
 // whole 128-byte pieces of eight rows, and a trade between lanes, against 64 bytes
 // of sixteen rows: 50.2 us, and 13 x 18944 x 3584 (68 MB) 16.1 against 19.1 (half
 // pieces ask for every line twice).
@@ -465,7 +465,7 @@ hipError_t launch_f8_gemm(const F8Args &a, hipStream_t s) {
     p.slices = pl.slices;
   }
   // Two launches, of which the scales let one have the work, pay from some 50 us
-  // on (4096 x 18944 x 3584 dB 889 -> 732 us with the gradient's kernel; the idle one
+  // on (4096 x 18944 x 3584 dB 889 -> 723 us with the gradient's kernel; the idle one
   // takes 4.7).
   if (static_cast<double>(a.M) * a.N * a.K < 4e10) p.powers = nullptr;
   switch (a.out) {
